@@ -7,8 +7,8 @@
  *  rc_alloc, rc_free, sched_order, rc_stats, rc_dump.  Plain C++ on the
  *  caller's thread; not thread-safe per cache object.
  *
- *  Device (hand-written CUDA for sm_103a): kv_store, attn_decode, attn_extend,
- *  their workspace queries, and rc_sync.  All device memory is the caller's:
+ *  Device (hand-written CUDA for sm_103a): kv_store, kv_store_rope, attn_decode,
+ *  attn_extend, attn_cross, their workspace queries, and rc_sync.  All device memory is the caller's:
  *  the library never allocates it (its one device array is the fixed scratch
  *  of attn_decode_static).  Device calls enqueue work on `stream` and
  *  return; an error detected inside a kernel (a slot index outside the pool)
@@ -294,7 +294,18 @@ rc_status bc_stats(bc_cache* cache, rc_stats_t* out);
  * group]: k and v hold E4M3 codes, one byte per element in the same
  * [n_slots][kv_heads][head_dim] layout, and k_scale / v_scale are fp32
  * [n_slots][kv_heads]; an element's value is its code times the scale of its
- * (slot, head) row.  kv_store quantises (see there); attn_decode reads it. */
+ * (slot, head) row.  kv_store quantises (see there); attn_decode reads it.
+ * 4-bit pool (kv_fp8 == RC_KV_FP4; GQA, head_dim 64 or 128; a library extra):
+ * a (slot, head) row of head_dim values is head_dim/16 blocks of 16.  k and v
+ * hold E2M1 codes, two per byte, the even element in the low half:
+ * [n_slots][kv_heads][head_dim/2] bytes; k_bscale and v_bscale hold a byte per
+ * block: [n_slots][kv_heads][head_dim/16], an unsigned float of 5 exponent
+ * bits (bias 15) and 3 mantissa bits, i.e. bits 14..7 of an f16.  An element's
+ * value is its code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times its
+ * block's scale, always an f16 value.  Scale byte 0xff is a NaN: its block's
+ * elements are NaN.  The four arrays are 16-byte aligned.  k_bscale and
+ * v_bscale are read for such a pool only. */
+#define RC_KV_FP4 4
 typedef struct rc_pool_desc {
     void* k;
     void* v;
@@ -307,6 +318,8 @@ typedef struct rc_pool_desc {
     int32_t kv_fp8;
     float* k_scale;
     float* v_scale;
+    uint8_t* k_bscale;
+    uint8_t* v_bscale;
 } rc_pool_desc;
 
 typedef struct rc_attn_desc {
@@ -339,11 +352,56 @@ typedef struct rc_kv_table {
  * e4m3(x_i / scale) (fp32 quotient rounded to nearest, then to the nearest
  * E4M3 value, ties to even, saturating at +-448); an all-zero row stores scale
  * 0 and zero codes.
+ * 4-bit pool: per block of 16, scale = amax|x| / 6 (fp32, rounded to nearest)
+ * rounded to the scale's 5 + 3 bits (nearest, ties to even, steps of 2^-17
+ * below 2^-14, at most 10240), and codes e2m1(x_i / scale) (fp32 quotient
+ * rounded to nearest, then to the nearest E2M1 value, ties to the even code,
+ * saturating at +-6; so values beyond 61440 saturate); a scale of 0 stores zero
+ * codes; a block with an infinity or a NaN stores scale byte 0xff.
  * Errors (host): RC_ERR_ARG, RC_ERR_UNSUPPORTED (row bytes not a multiple of 16;
  * an FP8 pool that is latent or whose head_dim is not 128), RC_ERR_CUDA (launch). */
 rc_status kv_store(const rc_pool_desc* pool, const int32_t* slots, const void* k_new,
                    const void* v_new, int32_t n, int32_t* table, const int32_t* table_pos,
                    rc_stream_t stream);
+
+/* Rotary positions for kv_store_rope.  cos_sin: device fp32
+ * [max_pos][rot_dim], for each position rot_dim/2 cosines, then rot_dim/2
+ * sines, 16-byte aligned.  Columns offset .. offset + rot_dim - 1 of every
+ * head row are rotated: pair j is (offset + j, offset + j + rot_dim/2), or with
+ * interleaved != 0 (offset + 2j, offset + 2j + 1); the others stay as they are. */
+typedef struct rc_rope_desc {
+    const float* cos_sin;
+    int32_t max_pos;
+    int32_t rot_dim;      /* a multiple of 32, at most head_dim */
+    int32_t offset;       /* a multiple of 16 */
+    int32_t interleaved;
+} rc_rope_desc;
+
+/* kv_store of n new tokens whose K still has to be rotated by its position,
+ * and the rotation of their Q, in one pass (a library extra: the pages leave
+ * positions to the model).  Pair (a, b) of token i becomes
+ * (a cos - b sin, b cos + a sin) with the angles of positions[i], in fp32 with
+ * every product and sum rounded once; K is then stored as kv_store stores a
+ * row of those fp32 values (a bf16 pool rounds them to nearest), V as it is.
+ * k_new, v_new, q: rows of kv_heads (q: q_heads) x head_dim bf16, the rows of
+ * neighbouring tokens k_stride, v_stride, q_stride elements apart (multiples
+ * of 8, so slices of one projection's output can be passed; 16-byte aligned).
+ * q_out: the rotated queries (bf16), rows q_out_stride apart (at least
+ * q_heads * head_dim); it may be q itself with the same stride, and then only
+ * the rotated columns are written, and must not overlap q otherwise.  q and
+ * q_out NULL: K and V only.  v_new is NULL for the latent layout, whose rows
+ * (one of 576 columns) rotate like the others.  slots, table, table_pos as in
+ * kv_store.  A token whose slot is outside [0, n_slots) stores no K and V (its
+ * Q is rotated), one whose position is outside [0, max_pos) nothing at all;
+ * both flag RC_ERR_DEVICE in pool->err.
+ * Errors (host): RC_ERR_ARG, RC_ERR_UNSUPPORTED (head_dim other than 64 and
+ * 128, or 576 latent; an FP8 pool's other than 128; rot_dim or offset not such
+ * multiples), RC_ERR_CUDA (launch). */
+rc_status kv_store_rope(const rc_pool_desc* pool, const rc_rope_desc* rope, const int32_t* slots,
+                        const int32_t* positions, const void* k_new, int64_t k_stride,
+                        const void* v_new, int64_t v_stride, int32_t n, const void* q,
+                        int64_t q_stride, int32_t q_heads, void* q_out, int64_t q_out_stride,
+                        int32_t* table, const int32_t* table_pos, rc_stream_t stream);
 
 /* Shared-prefix segments for cascade decode (all device arrays caller-owned;
  * the tree gives them: a node pinned by several running requests is one
@@ -493,6 +551,31 @@ rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
 rc_status attn_extend(const rc_attn_desc* desc, const void* q, const int32_t* qo_indptr,
                       const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out,
                       float* lse, void* ws, size_t ws_bytes, rc_stream_t stream);
+
+/* Workspace bytes attn_cross needs for this batch (0 unless keys are split). */
+rc_status attn_cross_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
+                               int32_t max_len, size_t* bytes);
+
+/* Cross attention (a library extra): new token i of row b attends to all the
+ * keys of the row's table, an encoder's states stored in the pool (by kv_store;
+ * as a run of image keys in the tree, they are shared like any prefix), which
+ * have no relation to the row's own tokens.  Row b has
+ * n_b = qo_indptr[b+1]-qo_indptr[b] tokens (0 <= n_b <= max_q) and len[b] keys
+ * (0 <= len[b] <= kv->max_len); a row without keys gives zeros and an lse of
+ * -infinity.  q and out: [sum n_b][q_heads][head_dim] bf16, 16-byte aligned;
+ * rows of out behind the last token are not written.  lse: NULL or
+ * [sum n_b][q_heads] fp32, natural log.  bf16, FP8 (head_dim 128) and 4-bit
+ * pools, head_dim 64 or 128, 1, 2, 4 or 8 query heads per KV head.
+ * ws: attn_cross_workspace bytes, 256-byte aligned (NULL when that is 0); calls
+ * that can overlap on the GPU need a workspace each.
+ * A row whose tokens exceed max_q, or reach beyond batch * max_q in all, is not
+ * computed, a row of keys outside the table or longer than max_len is taken as
+ * empty; both flag RC_ERR_DEVICE in the pool's err, as a slot outside the pool
+ * does (its key then reads as zeros).
+ * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED, RC_ERR_CUDA. */
+rc_status attn_cross(const rc_attn_desc* desc, const void* q, const int32_t* qo_indptr,
+                     const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out, float* lse,
+                     void* ws, size_t ws_bytes, rc_stream_t stream);
 
 /* Wait for `stream`, then read and clear the device error word `err` (may be
  * NULL).  A library extra (the pages have no counterpart): it is how errors

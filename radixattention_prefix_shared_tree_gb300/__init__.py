@@ -8,8 +8,8 @@ if the library is missing, loading it raises.
 
 Function names follow the header: ``rc_create``, ``rc_match_prefix``,
 ``rc_insert``, ``rc_release``, ``rc_evict``, ``rc_alloc``, ``rc_free``,
-``sched_order``, ``rc_stats``, ``rc_dump``, ``kv_store``, ``attn_decode``,
-``attn_extend``, ``rc_sync``.  ``RadixCache`` wraps a cache handle with the
+``sched_order``, ``rc_stats``, ``rc_dump``, ``kv_store``, ``kv_store_rope``,
+``attn_decode``, ``attn_extend``, ``attn_cross``, ``rc_sync``.  ``RadixCache`` wraps a cache handle with the
 host calls as methods.  Device calls take torch CUDA tensors (PyTorch is used
 for device memory and streams only).
 """
@@ -27,6 +27,7 @@ RC_ERR_CUDA, RC_ERR_TIMEOUT, RC_ERR_DEVICE, RC_ERR_UNSUPPORTED = -4, -5, -6, -7
 RC_ERR_SCRATCH = -8
 RC_STATIC_SCRATCH_BYTES = 32 << 20
 RC_FCFS, RC_LPM = 0, 1
+RC_KV_FP4 = 4
 
 I32, I64, VP = C.c_int32, C.c_int64, C.c_void_p
 P = C.POINTER
@@ -35,7 +36,11 @@ P = C.POINTER
 class rc_pool_desc(C.Structure):
     _fields_ = [("k", VP), ("v", VP), ("n_slots", I64), ("kv_heads", I32), ("head_dim_k", I32),
                 ("head_dim_v", I32), ("mla", I32), ("err", VP), ("kv_fp8", I32), ("k_scale", VP),
-                ("v_scale", VP)]
+                ("v_scale", VP), ("k_bscale", VP), ("v_bscale", VP)]
+
+
+class rc_rope_desc(C.Structure):
+    _fields_ = [("cos_sin", VP), ("max_pos", I32), ("rot_dim", I32), ("offset", I32), ("interleaved", I32)]
 
 
 class rc_attn_desc(C.Structure):
@@ -90,6 +95,8 @@ SIGNATURES = {
                               P(I32), P(I32)]),
     "rc_dump": (I32, [VP, C.c_char_p, I64, P(I64)]),
     "kv_store": (I32, [P(rc_pool_desc), VP, VP, VP, I32, VP, VP, VP]),
+    "kv_store_rope": (I32, [P(rc_pool_desc), P(rc_rope_desc), VP, VP, VP, I64, VP, I64, I32, VP, I64, I32, VP, I64, VP,
+                            VP, VP]),
     "attn_decode_workspace": (I32, [P(rc_attn_desc), I32, I32, P(rc_cascade), P(C.c_size_t)]),
     "attn_decode": (I32, [P(rc_attn_desc), VP, P(rc_kv_table), I32, P(rc_cascade), VP, VP, VP, C.c_size_t, VP]),
     "attn_decode_append": (I32, [P(rc_attn_desc), VP, VP, VP, P(rc_kv_table), I32, P(rc_cascade), VP, VP, VP,
@@ -99,6 +106,8 @@ SIGNATURES = {
     "attn_decode_static": (I32, [P(rc_attn_desc), VP, P(rc_kv_table), I32, P(rc_cascade), VP, VP, VP]),
     "attn_extend_workspace": (I32, [P(rc_attn_desc), I32, I32, I32, P(C.c_size_t)]),
     "attn_extend": (I32, [P(rc_attn_desc), VP, VP, P(rc_kv_table), I32, I32, VP, VP, VP, C.c_size_t, VP]),
+    "attn_cross_workspace": (I32, [P(rc_attn_desc), I32, I32, I32, P(C.c_size_t)]),
+    "attn_cross": (I32, [P(rc_attn_desc), VP, VP, P(rc_kv_table), I32, I32, VP, VP, VP, C.c_size_t, VP]),
     "rc_sync": (I32, [VP, VP]),
     "rc_probe_wait_timeout": (I32, [VP, VP]),
     "rc_strerror": (C.c_char_p, [I32]),
@@ -420,13 +429,25 @@ def _stream(stream):
 
 
 def make_pool_desc(k, v, err=None, mla: bool = False, head_dim_v: int | None = None, k_scale=None,
-                   v_scale=None) -> rc_pool_desc:
+                   v_scale=None, k_bscale=None, v_bscale=None) -> rc_pool_desc:
     """Descriptor of a pool held in torch tensors: k [n_slots, Hkv, dk] (or [n_slots, dk] latent).
     With k_scale / v_scale (fp32 [n_slots, Hkv]) the pool is FP8: k, v hold E4M3 codes (uint8).
+    With k_bscale / v_bscale (uint8 [n_slots, Hkv, d/16]) it is a 4-bit pool: k, v [n_slots, Hkv, d/2]
+    hold two E2M1 codes per byte (uint8).
     The kernels index the pool as dense row-major arrays, so every tensor must be contiguous."""
-    for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+    for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale), ("k_bscale", k_bscale),
+                    ("v_bscale", v_bscale)):
         if t is not None and not t.is_contiguous():
             raise ValueError(f"make_pool_desc: {name} must be contiguous (dense row-major [n_slots, ...])")
+    if (k_bscale is None) != (v_bscale is None) or (k_bscale is not None and (k_scale is not None or mla)):
+        raise ValueError("make_pool_desc: a 4-bit pool has k_bscale and v_bscale, and no k_scale, v_scale or mla")
+    if k_bscale is not None:
+        for name, t, s in (("k", k, k_bscale), ("v", v, v_bscale)):
+            if t.element_size() != 1 or s.element_size() != 1 or s.shape != (*t.shape[:2], t.shape[2] // 8):
+                raise ValueError(f"make_pool_desc: 4-bit {name} is uint8 [n_slots, Hkv, d/2] with scales uint8 "
+                                 f"[n_slots, Hkv, d/16], got {tuple(t.shape)} and {tuple(s.shape)}")
+        if v.shape[:2] != k.shape[:2]:
+            raise ValueError("make_pool_desc: k and v differ in slots or heads")
     d = rc_pool_desc()
     d.k = k.data_ptr()
     d.v = v.data_ptr() if v is not None else None
@@ -442,7 +463,11 @@ def make_pool_desc(k, v, err=None, mla: bool = False, head_dim_v: int | None = N
     if k_scale is not None:
         d.kv_fp8 = 1
         d.k_scale, d.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-    d._keep = (k, v, err, k_scale, v_scale)   # raw pointers inside: keep the tensors alive with it
+    if k_bscale is not None:
+        d.kv_fp8 = RC_KV_FP4
+        d.head_dim_k, d.head_dim_v = 2 * k.shape[2], 2 * v.shape[2]
+        d.k_bscale, d.v_bscale = k_bscale.data_ptr(), v_bscale.data_ptr()
+    d._keep = (k, v, err, k_scale, v_scale, k_bscale, v_bscale)   # raw pointers inside: keep the tensors alive with it
     return d
 
 
@@ -492,6 +517,68 @@ def kv_store(pool: rc_pool_desc, slots, k_new, v_new, table=None, table_pos=None
     st = lib().kv_store(C.byref(pool), _tp(slots), _tp(k_new), _tp(v_new), int(slots.numel()), _tp(table),
                         _tp(table_pos), _stream(stream))
     _check("kv_store", st)
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """cos_sin of make_rope_desc: fp32 [max_pos, rot_dim] of the angles
+    p * base^(-2j / rot_dim), j < rot_dim/2, taken in 64 bits (at position
+    100,000 a 32-bit angle is off by up to 0.004)."""
+    import torch
+    inv = float(base) ** (-torch.arange(0, int(rot_dim), 2, dtype=torch.float64, device=device) / int(rot_dim))
+    a = torch.arange(int(max_pos), dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], -1).to(torch.float32).contiguous()
+
+
+def make_rope_desc(cos_sin, interleaved: bool = False, offset: int = 0) -> rc_rope_desc:
+    """Rotary positions from a cos_sin tensor (fp32 [max_pos, rot_dim], see
+    rope_table): columns offset .. offset + rot_dim of every head row rotate."""
+    if cos_sin.dim() != 2 or cos_sin.element_size() != 4 or not cos_sin.is_floating_point() or \
+            not cos_sin.is_contiguous():
+        raise ValueError("make_rope_desc: cos_sin is a contiguous fp32 tensor [max_pos, rot_dim]")
+    r = rc_rope_desc()
+    r.cos_sin = cos_sin.data_ptr()
+    r.max_pos, r.rot_dim = cos_sin.shape
+    r.offset, r.interleaved = int(offset), int(bool(interleaved))
+    r._keep = (cos_sin,)
+    return r
+
+
+def _rows(name, t, n, heads, dim, write=False):
+    """(pointer, stride between tokens) of bf16 rows [n, heads, dim], each row
+    dense; tokens may be further apart (a slice of a projection's output)."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != dim or (heads and t.shape[1] != heads):
+        raise ValueError(f"{name}: expected [{n}, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    if t.element_size() != 2 or not t.is_floating_point():
+        raise ValueError(f"{name}: expected bf16, got {t.dtype}")
+    s0, s1, s2 = t.stride()
+    if n <= 1:
+        s0 = t.shape[1] * dim
+    if (dim > 1 and s2 != 1) or (t.shape[1] > 1 and s1 != dim):
+        raise ValueError(f"{name}: each token's rows must be dense, got strides {t.stride()}")
+    if write and s0 < t.shape[1] * dim:
+        raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
+    return C.c_void_p(t.data_ptr()), s0
+
+
+def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_new, v_new, q=None, q_out=None,
+                  table=None, table_pos=None, stream=None):
+    """Append n tokens with K (and Q) rotated by their positions (see the
+    header).  k_new, v_new [n, Hkv, d], q, q_out [n, Hq, d]: bf16, token strides
+    of their own; v_new None for a latent pool; q_out None rotates q in place.
+    slots, positions: int32 [n]."""
+    n, d = int(slots.numel()), pool.head_dim_k
+    if positions.numel() != n or slots.element_size() != 4 or positions.element_size() != 4:
+        raise ValueError("kv_store_rope: slots and positions are int32 of one length")
+    kp, ks = _rows("k_new", k_new, n, pool.kv_heads, d)
+    vp, vs = _rows("v_new", v_new, n, pool.kv_heads, d)
+    qp, qs = _rows("q", q, n, 0, d, write=q_out is None)
+    op, os_ = (qp, qs) if q_out is None else _rows("q_out", q_out, n, q.shape[1], d, write=True)
+    st = lib().kv_store_rope(C.byref(pool), C.byref(rope), _tp(slots), _tp(positions), kp, ks, vp, vs, n, qp, qs,
+                             0 if q is None else int(q.shape[1]), op, os_, _tp(table), _tp(table_pos),
+                             _stream(stream))
+    _check("kv_store_rope", st)
 
 
 def attn_decode_workspace(desc: rc_attn_desc, batch: int, max_len: int, cascade: rc_cascade | None = None) -> int:
@@ -563,6 +650,22 @@ def attn_extend(desc: rc_attn_desc, q, qo_indptr, kv: rc_kv_table, batch: int, m
                            _tp(lse), _tp(ws), int(ws.numel() * ws.element_size()) if ws is not None else 0,
                            _stream(stream))
     _check("attn_extend", st)
+
+
+def attn_cross_workspace(desc: rc_attn_desc, batch: int, max_q: int, max_len: int) -> int:
+    n = C.c_size_t(0)
+    _check("attn_cross_workspace", lib().attn_cross_workspace(C.byref(desc), int(batch), int(max_q), int(max_len),
+                                                               C.byref(n)))
+    return int(n.value)
+
+
+def attn_cross(desc: rc_attn_desc, q, qo_indptr, kv: rc_kv_table, batch: int, max_q: int, out, lse=None,
+               ws=None, stream=None):
+    """Every token of row b over all the keys of the row (see the header)."""
+    st = lib().attn_cross(C.byref(desc), _tp(q), _tp(qo_indptr), C.byref(kv), int(batch), int(max_q), _tp(out),
+                          _tp(lse), _tp(ws), int(ws.numel() * ws.element_size()) if ws is not None else 0,
+                          _stream(stream))
+    _check("attn_cross", st)
 
 
 def rc_sync(err=None, stream=None) -> int:

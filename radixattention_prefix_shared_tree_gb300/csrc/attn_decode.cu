@@ -20,475 +20,14 @@
 //  3. merge pass (split rows only): per (request, head), combine all
 //     partials by log-sum-exp.
 
+#include "attn_decode_fp4.cuh"
+#include "attn_decode_split.cuh"
 #include "attn_tc2.cuh"
 #include "common.cuh"
 
 namespace {
 
-constexpr int kDecKeys = 64;    // chunk sizes are multiples of this
-
-struct DecParams {
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* pool_k;
-    const __nv_bfloat16* pool_v;
-    int64_t n_slots;
-    int32_t kv_heads, q_heads;
-    float scale_log2;
-    int32_t* err;
-    const int32_t* table;
-    const int32_t* start;
-    const int32_t* len;
-    int64_t table_len;
-    int32_t chunk;       // keys per CTA
-    int32_t n_chunks;    // max chunks per request (partial stride)
-    float* part_o;       // [B][Hq][n_chunks][D]      (unfused)
-    float* part_lse;     // [B][Hq][n_chunks]
-    // fused epilogue: combine with the cascade partials and write the result
-    const float* seg_o;  // [total_seg_rows][Hq][seg_chunks][D]
-    const float* seg_lse;
-    const int32_t* req_seg_indptr;  // NULL: no cascade
-    const int32_t* req_seg_pos;
-    int32_t seg_chunks;
-    __nv_bfloat16* out;
-    float* lse;
-    // attn_decode_append: each row's last key comes from here and is stored
-    const __nv_bfloat16* k_new;  // [B][kv_heads][D] or NULL
-    const __nv_bfloat16* v_new;
-    // FP8 pool: pool_k / pool_v hold E4M3 codes, these the per-row scales
-    const float* k_scale;  // [n_slots][kv_heads]
-    const float* v_scale;
-};
-
-// Decode with one warp per item (request b, KV head, key chunk).  Each warp
-// streams its keys through a private ring of 16-key tiles (one m16 tile of
-// the swapped product) with cp.async, synchronising with __syncwarp only, so
-// the warps of an SM overlap each other's load latency and epilogues freely.
-// Wait until the grid this one depends on programmatically (the cascade
-// kernel) has finished and its writes are visible; returns at once when the
-// grid was launched without that dependency.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-
-constexpr int kWarpKeys = 16;
-constexpr int kWarpsPerCta = 14;  // one CTA per SM (14 x 16 KB + the CTA's 1 KB reserve fit; seven CTAs of
-constexpr int kCtasPerSm = 1;     // two warps would not): 2128 resident warps, the 2048 (row, KV head) items
-                                  // of a 256-row GQA-8 batch in one wave
-
-// Per-warp ring: S stages of one 16-key tile each (K then V, then for an FP8
-// pool the tile's 16 K scales and 16 V scales); a stage is refilled as soon
-// as its tile is reduced, so S tiles are in flight while the warp waits.
-template <bool FP8>
-__host__ __device__ constexpr int warp_stages() { return FP8 ? 3 : 2; }
-template <int D, bool FP8>
-__host__ __device__ constexpr int tile_bytes() { return kWarpKeys * D * (FP8 ? 1 : 2); }
-template <int D, bool FP8>
-__host__ __device__ constexpr int stage_bytes() { return 2 * tile_bytes<D, FP8>() + (FP8 ? 2 * kWarpKeys * 4 : 0); }
-template <int D, bool FP8>
-__host__ __device__ constexpr int warp_smem_bytes() {  // the K/V ring only (Q and slot ids in registers)
-    return warp_stages<FP8>() * stage_bytes<D, FP8>();
-}
-template <int D, bool FP8>
-__host__ __device__ constexpr int dec_smem_bytes() {
-    return kWarpsPerCta * warp_smem_bytes<D, FP8>();
-}
-
-template <int D, int G, bool FUSED, bool FP8>
-__global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_kernel(const DecParams p, int n_items) {
-    constexpr int ESZ = FP8 ? 1 : 2;                // bytes per K/V element
-    constexpr int CH = D * ESZ / 16;                // 16-byte chunks per row
-    constexpr int KS = D / 16;
-    constexpr int PER = kWarpKeys * CH / 32;        // chunks per lane per matrix
-    constexpr int S = warp_stages<FP8>();
-    constexpr int TILE_BYTES = tile_bytes<D, FP8>();
-    constexpr int STAGE_BYTES = stage_bytes<D, FP8>();
-    static_assert(kWarpKeys == 16, "slot ids: one lane per key");
-    static_assert(!FP8 || D == 128, "FP8 pools: head_dim 128");
-    // the epilogue reuses the ring: [8][D] fp32 outputs plus the merge scratch
-    static_assert(warp_smem_bytes<D, FP8>() >= 8 * D * 4 + 32 + 32 * 8 + G * 32 * 4 + G * 8, "epilogue scratch");
-    extern __shared__ __align__(128) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g_lane = lane >> 2, t_lane = lane & 3;
-    // the next step's cascade kernel (launched as this grid's dependent) may
-    // take SMs as they free up: it waits for this grid's end itself
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const int it = blockIdx.x * kWarpsPerCta + warp;
-    if (it >= n_items) {
-        grid_dep_wait();
-        return;
-    }
-    unsigned char* wbase = smem + warp * warp_smem_bytes<D, FP8>();
-
-    const int kvh = it % p.kv_heads;
-    const int rest = it / p.kv_heads;
-    const int chunk = rest % p.n_chunks;
-    const int b = rest / p.n_chunks;
-    const int64_t row0 = p.start[b];
-    int L = p.len[b];
-    if (row0 < 0 || L < 0 || row0 + L > p.table_len) {  // row outside the table: read nothing
-        if (lane == 0 && kvh == 0 && chunk == 0) rc::flag_error(p.err, rc::kErrBadSlot);
-        L = 0;
-    }
-    if (FUSED && lane == 0 && kvh == 0 && L > p.chunk) rc::flag_error(p.err, rc::kErrBadSlot);
-    const int k0 = chunk * p.chunk;
-    const int count = max(0, min(L - k0, p.chunk));
-    if (!FUSED && count == 0) {
-        grid_dep_wait();
-        return;
-    }
-    const int32_t* keys = p.table + row0 + k0;
-    const int n_tiles = (count + kWarpKeys - 1) / kWarpKeys;
-    // fused epilogue: the cascade partials this row folds in; the row offsets
-    // of the first 32 (lane j: partial j) are read now, ahead of the main loop
-    // (the segment tables are the caller's inputs, not the cascade's output)
-    int e0 = 0, n_parts = 0;
-    if (FUSED && p.req_seg_indptr) {
-        e0 = p.req_seg_indptr[b];
-        n_parts = (p.req_seg_indptr[b + 1] - e0) * p.seg_chunks;
-    }
-    auto part_row = [&](int j) -> int64_t {
-        return j < n_parts ? (int64_t)p.req_seg_pos[e0 + j / p.seg_chunks] * p.q_heads * p.seg_chunks +
-                                 (j % p.seg_chunks)
-                           : 0;
-    };
-    const int64_t first_row = part_row(lane);
-    // attn_decode_append: the row's last key (position L-1) is the step's new
-    // token.  The warp whose keys hold it gathers it from k_new/v_new and
-    // writes it to its pool slot (lanes 0..CH-1 the K row, CH..2CH-1 the V row).
-    const int new_at = (!FP8 && p.k_new && L > 0 && L - 1 >= k0 && L - 1 < k0 + count) ? L - 1 - k0 : -1;
-    if (new_at >= 0) {
-        const int slot = keys[new_at];
-        if (slot < 0 || (int64_t)slot >= p.n_slots) {
-            if (lane == 0) rc::flag_error(p.err, rc::kErrBadSlot);
-        } else if (lane < 2 * CH) {
-            const int c = lane % CH;
-            const int64_t off = ((int64_t)slot * p.kv_heads + kvh) * D + c * 8;
-            const int64_t src = ((int64_t)b * p.kv_heads + kvh) * D + c * 8;
-            if (lane < CH)
-                *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.pool_k) + off) =
-                    *reinterpret_cast<const uint4*>(p.k_new + src);
-            else
-                *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.pool_v) + off) =
-                    *reinterpret_cast<const uint4*>(p.v_new + src);
-        }
-    }
-
-    // Slot ids are prefetched into registers one tile ahead: lane l (and
-    // l + 16) holds the slot of key l of a tile.
-    auto slot_of = [&](int t) -> int {
-        const int key = t * kWarpKeys + (lane & 15);
-        return (t < n_tiles && key < count) ? __ldg(keys + key) : 0;
-    };
-    // a request's own keys are read once per step: they should not push the
-    // shared prefix (read by the cascade kernel every step) out of L2
-    const uint64_t pol = rc::l2_policy_evict_first();
-    auto issue = [&](int t, int tslots) {
-        if (t < n_tiles) {
-            unsigned char* sK = wbase + (t % S) * STAGE_BYTES;
-            unsigned char* sV = sK + TILE_BYTES;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int lin = i * 32 + lane;
-                const int r = lin / CH, c = lin % CH;
-                const int slot = __shfl_sync(0xffffffffu, tslots, r);
-                uint32_t bytes = 16;
-                const unsigned char* bk = reinterpret_cast<const unsigned char*>(p.pool_k);
-                const unsigned char* bv = reinterpret_cast<const unsigned char*>(p.pool_v);
-                int64_t row = 0;
-                if (t * kWarpKeys + r >= count) bytes = 0;
-                else if (t * kWarpKeys + r == new_at) {  // the appended key, straight from its source
-                    bk = reinterpret_cast<const unsigned char*>(p.k_new);
-                    bv = reinterpret_cast<const unsigned char*>(p.v_new);
-                    row = b;
-                } else if (slot < 0 || (int64_t)slot >= p.n_slots) {
-                    rc::flag_error(p.err, rc::kErrBadSlot);
-                    bytes = 0;
-                } else {
-                    row = slot;
-                }
-                const int64_t roff = (row * p.kv_heads + kvh) * (D * ESZ) + c * 16;
-                rc::cp_async16(rc::smem_u32(sK + rc::swz<CH>(r, c)), bk + roff, bytes, pol);
-                rc::cp_async16(rc::smem_u32(sV + rc::swz<CH>(r, c)), bv + roff, bytes, pol);
-            }
-            if constexpr (FP8) {  // lanes 0-15: K scale of key lane, 16-31: V scale of key lane-16
-                const int r = lane & 15;
-                const bool ok = t * kWarpKeys + r < count && tslots >= 0 && (int64_t)tslots < p.n_slots;
-                const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (int64_t)tslots * p.kv_heads + kvh : 0);
-                rc::cp_async4(rc::smem_u32(sV + TILE_BYTES + lane * 4), src, ok ? 4u : 0u);
-            }
-        }
-    };
-    // prologue: slot ids of tiles 0 and 1, K/V of tile 0, and the Q operand
-    // fragments straight from global memory (head g_lane of this KV head's
-    // group, zero for g_lane >= G; two bf16 per register, as ldmatrix would
-    // give them)
-    // Tiles t..t+S-1 are in flight while the warp waits for tile t; tile
-    // t+S goes into tile t's stage as soon as tile t has been reduced.
-    int cur = slot_of(S), nxt;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        issue(i, slot_of(i));
-        rc::cp_async_commit();
-    }
-    uint32_t qb[KS][2];
-    {
-        const bool hv = g_lane < G;
-        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
-            p.q + ((int64_t)b * p.q_heads + kvh * G + (hv ? g_lane : 0)) * D);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if constexpr (FP8) {
-                // f16 operands, and k-step ks takes dims 16ks+4t..16ks+4t+3 of
-                // this lane's K words (see below): the same dims of Q
-                qb[ks][0] = hv ? rc::bf16x2_to_f16x2(__ldg(qrow + ks * 8 + 2 * t_lane)) : 0u;
-                qb[ks][1] = hv ? rc::bf16x2_to_f16x2(__ldg(qrow + ks * 8 + 2 * t_lane + 1)) : 0u;
-            } else {
-                qb[ks][0] = hv ? __ldg(qrow + ks * 8 + t_lane) : 0u;
-                qb[ks][1] = hv ? __ldg(qrow + ks * 8 + 4 + t_lane) : 0u;
-            }
-        }
-    }
-    float o[KS][4];
-#pragma unroll
-    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-
-    for (int t = 0; t < n_tiles; ++t) {
-        rc::cp_async_wait<S - 1>();  // tile t landed (later tiles may still be in flight)
-        __syncwarp();
-        nxt = slot_of(t + S + 1);
-        const unsigned char* sK = wbase + (t % S) * STAGE_BYTES;
-        const unsigned char* sV = sK + TILE_BYTES;
-        const float* sSc = reinterpret_cast<const float*>(sV + TILE_BYTES);  // FP8: K scales, then V scales
-        // S^T (16 keys x 8 heads) = K Q^T, even and odd k-steps in two
-        // accumulators (two independent chains of MMAs)
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-            float s2[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (FP8) {
-                // A fragment from E4M3 words: row g (and g+8), 16-byte chunk ks,
-                // word t_lane = dims 16ks+4t..+3; the k-step's columns 2t, 2t+1
-                // take the word's first two dims, 2t+8, 2t+9 the last two
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(sK + rc::swz<CH>(g_lane, ks) + 4 * t_lane);
-                    const uint32_t w1 =
-                        *reinterpret_cast<const uint32_t*>(sK + rc::swz<CH>(g_lane + 8, ks) + 4 * t_lane);
-                    uint32_t a0, a1, a2, a3;
-                    rc::e4m3x4_to_f16x4(w0, a0, a2);
-                    rc::e4m3x4_to_f16x4(w1, a1, a3);
-                    rc::mma_f16_16816(ks & 1 ? s2 : s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
-                }
-            } else {
-                const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t a0, a1, a2, a3;
-                    rc::ldmatrix_x4(rc::smem_u32(sK + rc::swz<CH>(key, ks * 2 + (lane >> 4))), a0, a1, a2, a3);
-                    rc::mma_bf16_16816(ks & 1 ? s2 : s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += s2[i];
-            if constexpr (FP8) {  // code products times the keys' scales
-                const float k_lo = sSc[g_lane], k_hi = sSc[g_lane + 8];
-                s[0] *= k_lo;
-                s[1] *= k_lo;
-                s[2] *= k_hi;
-                s[3] *= k_hi;
-            }
-        }
-        const int key_lo = t * kWarpKeys + g_lane;
-        const bool v_lo = key_lo < count, v_hi = key_lo + 8 < count;
-        s[0] = v_lo ? s[0] * p.scale_log2 : -INFINITY;
-        s[1] = v_lo ? s[1] * p.scale_log2 : -INFINITY;
-        s[2] = v_hi ? s[2] * p.scale_log2 : -INFINITY;
-        s[3] = v_hi ? s[3] * p.scale_log2 : -INFINITY;
-        // Online softmax with a lazy reference: exponentials are taken
-        // against m_run, which moves (rescaling O and l) only when a head's
-        // max grows past it by more than 2^8 -- the terms stay below 2^8, and
-        // most tiles skip the 32 multiplies of the rescale.
-        float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-        float alpha[2] = {1.f, 1.f};
-        bool grow = false;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
-            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
-            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-            if (mx[j] > m_run[j] + 8.f) {
-                alpha[j] = rc::fast_exp2(m_run[j] - mx[j]);  // 0 while nothing was seen
-                m_run[j] = mx[j];
-                grow = true;
-            }
-        }
-        const float mu0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float mu1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
-        const float p0 = rc::fast_exp2(s[0] - mu0), p1 = rc::fast_exp2(s[1] - mu1);
-        const float p2 = rc::fast_exp2(s[2] - mu0), p3 = rc::fast_exp2(s[3] - mu1);
-        if (__any_sync(0xffffffffu, grow)) {
-            l_run[0] *= alpha[0];
-            l_run[1] *= alpha[1];
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                o[i][0] *= alpha[0];
-                o[i][1] *= alpha[1];
-                o[i][2] *= alpha[0];
-                o[i][3] *= alpha[1];
-            }
-        }
-        l_run[0] += p0 + p2;
-        l_run[1] += p1 + p3;
-        if constexpr (FP8) {
-            // P times the values' scales (f16), then O^T += V^T P^T with V^T
-            // built from E4M3 bytes: this lane reads 16-byte chunk g of keys
-            // 2t, 2t+1, 2t+8, 2t+9 (dims 16g..16g+15); product mt uses dims
-            // 16g+2mt (row g) and 16g+2mt+1 (row g+8), paired across keys
-            // with a byte permute
-            const float v_lo = sSc[kWarpKeys + g_lane], v_hi = sSc[kWarpKeys + g_lane + 8];
-            const uint32_t pb0 = rc::movmatrix_trans(rc::pack_f16(p0 * v_lo, p1 * v_lo));
-            const uint32_t pb1 = rc::movmatrix_trans(rc::pack_f16(p2 * v_hi, p3 * v_hi));
-            const uint4 w0 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane, g_lane));
-            const uint4 w1 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane + 1, g_lane));
-            const uint4 w8 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane + 8, g_lane));
-            const uint4 w9 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane + 9, g_lane));
-            const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-            const uint32_t x8[4] = {w8.x, w8.y, w8.z, w8.w}, x9[4] = {w9.x, w9.y, w9.z, w9.w};
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
-                uint32_t a0, a1, a2, a3;
-                rc::e4m3x4_to_f16x4(rc::prmt(x0[mt >> 1], x1[mt >> 1], sel), a0, a1);
-                rc::e4m3x4_to_f16x4(rc::prmt(x8[mt >> 1], x9[mt >> 1], sel), a2, a3);
-                rc::mma_f16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
-            }
-        } else {
-            const uint32_t pb0 = rc::movmatrix_trans(rc::pack_bf16(p0, p1));
-            const uint32_t pb1 = rc::movmatrix_trans(rc::pack_bf16(p2, p3));
-            const int key = (lane & 7) + (lane >> 4) * 8;
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                uint32_t a0, a1, a2, a3;
-                rc::ldmatrix_x4_trans(rc::smem_u32(sV + rc::swz<CH>(key, mt * 2 + ((lane >> 3) & 1))), a0, a1, a2,
-                                      a3);
-                rc::mma_bf16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
-            }
-        }
-        __syncwarp();  // every lane has read tile t: its stage takes tile t+S
-        issue(t + S, cur);
-        rc::cp_async_commit();
-        cur = nxt;
-    }
-    rc::cp_async_wait<0>();
-    __syncwarp();
-
-    // ---------------------------------------------------------- epilogue
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 4);
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 8);
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 16);
-    }
-    // this warp's normalised output per (head, dim) into its (now free) ring
-    float* sE = reinterpret_cast<float*>(wbase);           // [8][D]
-    float* sOwn = sE + 8 * D;                               // [8] log2-sum-exp per head
-    const float inv0 = l_run[0] > 0.f ? 1.f / l_run[0] : 0.f;
-    const float inv1 = l_run[1] > 0.f ? 1.f / l_run[1] : 0.f;
-#pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
-        // accumulator rows g and g+8 of product mt: dims d0 and d1
-        const int d0 = FP8 ? 16 * g_lane + 2 * mt : mt * 16 + g_lane;
-        const int d1 = FP8 ? d0 + 1 : d0 + 8;
-        sE[(2 * t_lane) * D + d0] = o[mt][0] * inv0;
-        sE[(2 * t_lane + 1) * D + d0] = o[mt][1] * inv1;
-        sE[(2 * t_lane) * D + d1] = o[mt][2] * inv0;
-        sE[(2 * t_lane + 1) * D + d1] = o[mt][3] * inv1;
-    }
-    if (g_lane == 0) {
-        sOwn[2 * t_lane] = l_run[0] > 0.f ? m_run[0] + log2f(l_run[0]) : -INFINITY;
-        sOwn[2 * t_lane + 1] = l_run[1] > 0.f ? m_run[1] + log2f(l_run[1]) : -INFINITY;
-    }
-    __syncwarp();
-    // The cascade kernel, when there is one, may still be running (this
-    // grid is its programmatic dependent): wait for it before reading its
-    // partials, and in any case before leaving, so that the end of this grid
-    // implies the end of both.
-    grid_dep_wait();
-    if constexpr (!FUSED) {
-        for (int h = 0; h < G; ++h) {
-            const int64_t idx = ((int64_t)b * p.q_heads + kvh * G + h) * p.n_chunks + chunk;
-            for (int d = lane; d < D; d += 32) p.part_o[idx * D + d] = sE[h * D + d];
-            if (lane == 0) p.part_lse[idx] = sOwn[h];
-        }
-    } else {
-        // the row's whole table part is here: fold in its cascade partials
-        // (every chunk of every segment it reads; partial j of head h sits at
-        // row part_row(j) + (kvh * G + h) * seg_chunks).  Partials come in
-        // batches of 32: lane j loads partial j's G log-sum-exps in one
-        // round, then every lane loads the batch's rows in a second round
-        // (all independent loads), merged online against a running max.
-        constexpr int kPB = 32;
-        int64_t* sRow = reinterpret_cast<int64_t*>(sOwn + 8);   // [kPB]
-        float* sL = reinterpret_cast<float*>(sRow + kPB);         // [G][kPB]
-        const int sc = p.seg_chunks;
-        float m_h[G], w_h[G], acc[G][D / 32];
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            m_h[h] = sOwn[h];
-            w_h[h] = sOwn[h] == -INFINITY ? 0.f : 1.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) acc[h][k] = m_h[h] == -INFINITY ? 0.f : sE[h * D + lane + 32 * k];
-        }
-        // none after a cascade kernel gave up on a bounded wait (unwritten)
-        const int n_use = (p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout)) ? 0 : n_parts;
-        for (int j0 = 0; j0 < n_use; j0 += kPB) {
-            const int nb = min(kPB, n_use - j0);
-            const int64_t my_row = j0 == 0 ? first_row : part_row(j0 + lane);
-            if (lane < nb) {
-                sRow[lane] = my_row;
-#pragma unroll
-                for (int h = 0; h < G; ++h) sL[h * kPB + lane] = p.seg_lse[my_row + (int64_t)(kvh * G + h) * sc];
-            }
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < G; ++h) {
-                float mb = m_h[h];
-                for (int j = 0; j < nb; ++j) mb = fmaxf(mb, sL[h * kPB + j]);
-                if (mb == -INFINITY) continue;   // nothing yet for this head
-                const float a = m_h[h] == -INFINITY ? 0.f : rc::fast_exp2(m_h[h] - mb);
-                w_h[h] *= a;
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) acc[h][k] *= a;
-                m_h[h] = mb;
-            }
-#pragma unroll 4
-            for (int j = 0; j < nb; ++j) {
-                const int64_t row = sRow[j];
-#pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const float l2 = sL[h * kPB + j];
-                    const float wj = l2 == -INFINITY ? 0.f : rc::fast_exp2(l2 - m_h[h]);
-                    w_h[h] += wj;
-                    const float* src = p.seg_o + (row + (int64_t)(kvh * G + h) * sc) * D + lane;
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        const float v = src[32 * k];
-                        acc[h][k] += wj == 0.f ? 0.f : wj * v;
-                    }
-                }
-            }
-            __syncwarp();
-        }
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const int64_t orow = (int64_t)b * p.q_heads + kvh * G + h;
-            const float inv = w_h[h] > 0.f ? 1.f / w_h[h] : 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-                p.out[orow * D + lane + 32 * k] = __float2bfloat16_rn(acc[h][k] * inv);
-            if (p.lse && lane == 0)
-                p.lse[orow] = w_h[h] > 0.f ? (m_h[h] + log2f(w_h[h])) * rc::kLn2 : -INFINITY;
-        }
-    }
-}
+using namespace rc_dec;
 
 // Combine every partial of (request, head): cascade segments (all chunks)
 // then the chunks of the request's own table row.
@@ -606,9 +145,10 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
     // tiles, about 2.5 us per 16 keys when the gather saturates HBM, so the
     // wave's longest item sets the call), down to 64 keys per chunk.
     const int64_t base = (int64_t)batch * hkv;
+    const int64_t warps = rc_host::pool_format(d->pool) == rc::kFmtFp4 ? fp4::kWarps : kWarpsPerCta;
     int64_t splits = 1;
     if (base < 8 * sms) {
-        splits = base > 0 ? (kWarpsPerCta * sms) / base : 1;
+        splits = base > 0 ? (warps * sms) / base : 1;
         const int64_t max_splits = max_len > 0 ? (max_len + kDecKeys - 1) / kDecKeys : 1;
         if (splits > max_splits) splits = max_splits;
         if (splits < 1) splits = 1;
@@ -657,20 +197,19 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
 // after_cascade: launched as the programmatic dependent of the cascade kernel
 // just queued on the stream, so that its CTAs start on SMs the cascade leaves
 // free and as cascade CTAs finish, instead of after the whole cascade grid.
-template <int D, int G, bool FUSED, bool FP8>
-cudaError_t launch_split(const DecParams& p, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
-    constexpr int smem = dec_smem_bytes<D, FP8>();
-    cudaError_t e = rc_host::ensure_smem<decode_split_kernel<D, G, FUSED, FP8>>(smem);
+template <auto Kernel, int WARPS>
+cudaError_t launch_table(const DecParams& p, int smem, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
+    cudaError_t e = rc_host::ensure_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
     const int n_items = batch * kv_heads * p.n_chunks;
-    const int grid = (n_items + kWarpsPerCta - 1) / kWarpsPerCta;
+    const int grid = (n_items + WARPS - 1) / WARPS;
     if (!after_cascade) {
-        decode_split_kernel<D, G, FUSED, FP8><<<grid, 32 * kWarpsPerCta, smem, st>>>(p, n_items);
+        Kernel<<<grid, 32 * WARPS, smem, st>>>(p, n_items);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(32 * kWarpsPerCta);
+    cfg.blockDim = dim3(32 * WARPS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -678,13 +217,23 @@ cudaError_t launch_split(const DecParams& p, int batch, int kv_heads, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, G, FUSED, FP8>, p, n_items);
+    return cudaLaunchKernelEx(&cfg, Kernel, p, n_items);
 }
 
-template <int D, int G, bool FP8>
+template <int D, int G, bool FUSED, int FMT>
+cudaError_t launch_split(const DecParams& p, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
+    if constexpr (FMT == rc::kFmtFp4)
+        return launch_table<decode_fp4_kernel<D, G, FUSED, false>, fp4::kWarps>(p, fp4::smem_bytes<D>(), batch,
+                                                                               kv_heads, st, after_cascade);
+    else
+        return launch_table<decode_split_kernel<D, G, FUSED, FMT == rc::kFmtFp8>, kWarpsPerCta>(
+            p, dec_smem_bytes<D, FMT == rc::kFmtFp8>(), batch, kv_heads, st, after_cascade);
+}
+
+template <int D, int G, int FMT>
 cudaError_t launch_cascade(const rc::MQParams& p0, const rc_cascade* c, int kv_heads, cudaStream_t st) {
-    constexpr int smem = rc_tc2::smem_bytes<D, FP8>();
-    cudaError_t e = rc_host::ensure_smem<rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCascade, FP8>>(smem);
+    constexpr int smem = rc_tc2::smem_bytes<D, FMT>();
+    cudaError_t e = rc_host::ensure_smem<rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCascade, FMT>>(smem);
     if (e != cudaSuccess) return e;
     constexpr int TPC = rc_tc2::ROWS / G;
     rc::MQParams p = p0;
@@ -720,37 +269,29 @@ cudaError_t launch_cascade(const rc::MQParams& p0, const rc_cascade* c, int kv_h
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCascade, FP8>, p);
+    return cudaLaunchKernelEx(&cfg, rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCascade, FMT>, p);
 }
 
-template <int D, int G>
-cudaError_t run_gqa(const DecParams& dp, const rc::MQParams& mp, const rc_cascade* casc, bool fused, bool fp8,
-                    int batch, int kv_heads, cudaStream_t st) {
+template <int D, int G, int FMT>
+cudaError_t run_gqa(const DecParams& dp, const rc::MQParams& mp, const rc_cascade* casc, bool fused, int batch,
+                    int kv_heads, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const bool with_cascade = casc && casc->n_seg > 0 && casc->max_seg_rows > 0;
-    if constexpr (D == 128) {
-        if (fp8) {
-            if (with_cascade) e = launch_cascade<D, G, true>(mp, casc, kv_heads, st);
-            if (e != cudaSuccess) return e;
-            return fused ? launch_split<D, G, true, true>(dp, batch, kv_heads, st, with_cascade)
-                         : launch_split<D, G, false, true>(dp, batch, kv_heads, st, with_cascade);
-        }
-    }
-    if (with_cascade) e = launch_cascade<D, G, false>(mp, casc, kv_heads, st);
+    if (with_cascade) e = launch_cascade<D, G, FMT>(mp, casc, kv_heads, st);
     if (e != cudaSuccess) return e;
-    return fused ? launch_split<D, G, true, false>(dp, batch, kv_heads, st, with_cascade)
-                 : launch_split<D, G, false, false>(dp, batch, kv_heads, st, with_cascade);
+    return fused ? launch_split<D, G, true, FMT>(dp, batch, kv_heads, st, with_cascade)
+                 : launch_split<D, G, false, FMT>(dp, batch, kv_heads, st, with_cascade);
 }
 
-template <int D>
+template <int D, int FMT>
 cudaError_t dispatch_group(int G, const DecParams& dp, const rc::MQParams& mp, const rc_cascade* casc, bool fused,
-                           bool fp8, int batch, int kv_heads, cudaStream_t st, bool* ok) {
+                           int batch, int kv_heads, cudaStream_t st, bool* ok) {
     *ok = true;
     switch (G) {
-        case 1: return run_gqa<D, 1>(dp, mp, casc, fused, fp8, batch, kv_heads, st);
-        case 2: return run_gqa<D, 2>(dp, mp, casc, fused, fp8, batch, kv_heads, st);
-        case 4: return run_gqa<D, 4>(dp, mp, casc, fused, fp8, batch, kv_heads, st);
-        case 8: return run_gqa<D, 8>(dp, mp, casc, fused, fp8, batch, kv_heads, st);
+        case 1: return run_gqa<D, 1, FMT>(dp, mp, casc, fused, batch, kv_heads, st);
+        case 2: return run_gqa<D, 2, FMT>(dp, mp, casc, fused, batch, kv_heads, st);
+        case 4: return run_gqa<D, 4, FMT>(dp, mp, casc, fused, batch, kv_heads, st);
+        case 8: return run_gqa<D, 8, FMT>(dp, mp, casc, fused, batch, kv_heads, st);
         default: *ok = false; return cudaSuccess;
     }
 }
@@ -801,17 +342,24 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     const rc_pool_desc& P = desc->pool;
     const int D = P.head_dim_k;
     if (P.mla || P.head_dim_v != D || !P.v) return RC_ERR_UNSUPPORTED;
-    const bool fp8 = P.kv_fp8 != 0;
+    const int fmt = rc_host::pool_format(P);
+    const bool fp8 = fmt == rc::kFmtFp8;
     if (fp8) {  // E4M3 pool: the table pass and the cascade read codes and scales
         if (D != 128 || k_new) return RC_ERR_UNSUPPORTED;
         if (!P.k_scale || !P.v_scale) return RC_ERR_ARG;
         if (use_casc && !rc_tc2::fp8_cascade_supported()) return RC_ERR_UNSUPPORTED;
     }
+    if (fmt == rc::kFmtFp4) {
+        if (k_new) return RC_ERR_UNSUPPORTED;
+        s = rc_host::check_fp4(P);
+        if (s != RC_OK) return s;
+        if (reinterpret_cast<uintptr_t>(q) & 15) return RC_ERR_ARG;
+    }
     const int G = desc->q_heads / P.kv_heads;
     unsigned char* w = static_cast<unsigned char*>(ws);
     float* seg_o = reinterpret_cast<float*>(w + pl.tail_o + pl.tail_lse);
     float* seg_lse = reinterpret_cast<float*>(w + pl.tail_o + pl.tail_lse + pl.seg_o);
-    DecParams dp;
+    DecParams dp{};
     dp.q = static_cast<const __nv_bfloat16*>(q);
     dp.pool_k = static_cast<const __nv_bfloat16*>(P.k);
     dp.pool_v = static_cast<const __nv_bfloat16*>(P.v);
@@ -839,6 +387,9 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     dp.v_new = static_cast<const __nv_bfloat16*>(v_new);
     dp.k_scale = fp8 ? P.k_scale : nullptr;
     dp.v_scale = fp8 ? P.v_scale : nullptr;
+    dp.k_bscale = fmt == rc::kFmtFp4 ? P.k_bscale : nullptr;
+    dp.v_bscale = fmt == rc::kFmtFp4 ? P.v_bscale : nullptr;
+    dp.group = G;
     rc::MQParams mp{};
     mp.q = dp.q;
     mp.pool_k = dp.pool_k;
@@ -850,6 +401,8 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     mp.err = dp.err;
     mp.k_scale = dp.k_scale;
     mp.v_scale = dp.v_scale;
+    mp.k_bscale = dp.k_bscale;
+    mp.v_bscale = dp.v_bscale;
     if (use_casc) {
         mp.seg_slots = casc->seg_slots;
         mp.seg_indptr = casc->seg_indptr;
@@ -865,8 +418,16 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     bool ok = false;
     cudaError_t e = cudaSuccess;
     const rc_cascade* cc = use_casc ? casc : nullptr;
-    if (D == 128) e = dispatch_group<128>(G, dp, mp, cc, pl.fused, fp8, batch, P.kv_heads, st, &ok);
-    else if (D == 64) e = dispatch_group<64>(G, dp, mp, cc, pl.fused, false, batch, P.kv_heads, st, &ok);
+    if (fmt == rc::kFmtFp4) {
+        if (D == 128) e = dispatch_group<128, rc::kFmtFp4>(G, dp, mp, cc, pl.fused, batch, P.kv_heads, st, &ok);
+        else e = dispatch_group<64, rc::kFmtFp4>(G, dp, mp, cc, pl.fused, batch, P.kv_heads, st, &ok);
+    } else if (fp8) {
+        e = dispatch_group<128, rc::kFmtFp8>(G, dp, mp, cc, pl.fused, batch, P.kv_heads, st, &ok);
+    } else if (D == 128) {
+        e = dispatch_group<128, rc::kFmtBf16>(G, dp, mp, cc, pl.fused, batch, P.kv_heads, st, &ok);
+    } else if (D == 64) {
+        e = dispatch_group<64, rc::kFmtBf16>(G, dp, mp, cc, pl.fused, batch, P.kv_heads, st, &ok);
+    }
     if (!ok) return RC_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return RC_ERR_CUDA;
     if (pl.fused) return RC_OK;

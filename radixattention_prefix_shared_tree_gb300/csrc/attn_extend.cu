@@ -17,34 +17,25 @@
 
 namespace {
 
-template <int D, int G, bool FP8>
+template <int D, int G, int FMT>
 cudaError_t launch_extend(const rc::MQParams& p, int batch, int max_q, int kv_heads, cudaStream_t st) {
-    constexpr int smem = rc_tc2::smem_bytes<D, FP8>();
-    cudaError_t e = rc_host::ensure_smem<rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FP8>>(smem);
+    constexpr int smem = rc_tc2::smem_bytes<D, FMT>();
+    cudaError_t e = rc_host::ensure_smem<rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT>>(smem);
     if (e != cudaSuccess) return e;
     constexpr int TPC = rc_tc2::ROWS / G;
     dim3 grid((max_q + TPC - 1) / TPC, kv_heads, batch);
-    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FP8><<<grid, rc_tc2::THREADS, smem, st>>>(p);
+    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT><<<grid, rc_tc2::THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-template <int D, int G>
-cudaError_t launch_extend_any(const rc::MQParams& p, bool fp8, int batch, int max_q, int kv_heads, cudaStream_t st) {
-    if constexpr (D == 128) {
-        if (fp8) return launch_extend<D, G, true>(p, batch, max_q, kv_heads, st);
-    }
-    return launch_extend<D, G, false>(p, batch, max_q, kv_heads, st);
-}
-
-template <int D>
-cudaError_t dispatch(int G, const rc::MQParams& p, bool fp8, int batch, int max_q, int kv_heads, cudaStream_t st,
-                     bool* ok) {
+template <int D, int FMT>
+cudaError_t dispatch(int G, const rc::MQParams& p, int batch, int max_q, int kv_heads, cudaStream_t st, bool* ok) {
     *ok = true;
     switch (G) {
-        case 1: return launch_extend_any<D, 1>(p, fp8, batch, max_q, kv_heads, st);
-        case 2: return launch_extend_any<D, 2>(p, fp8, batch, max_q, kv_heads, st);
-        case 4: return launch_extend_any<D, 4>(p, fp8, batch, max_q, kv_heads, st);
-        case 8: return launch_extend_any<D, 8>(p, fp8, batch, max_q, kv_heads, st);
+        case 1: return launch_extend<D, 1, FMT>(p, batch, max_q, kv_heads, st);
+        case 2: return launch_extend<D, 2, FMT>(p, batch, max_q, kv_heads, st);
+        case 4: return launch_extend<D, 4, FMT>(p, batch, max_q, kv_heads, st);
+        case 8: return launch_extend<D, 8, FMT>(p, batch, max_q, kv_heads, st);
         default: *ok = false; return cudaSuccess;
     }
 }
@@ -69,9 +60,15 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
     const rc_pool_desc& P = desc->pool;
     if (P.kv_heads <= 0 || desc->q_heads <= 0 || desc->q_heads % P.kv_heads) return RC_ERR_ARG;
     if (P.mla || !P.v || P.head_dim_v != P.head_dim_k) return RC_ERR_UNSUPPORTED;
-    const bool fp8 = P.kv_fp8 != 0;
+    const int fmt = rc_host::pool_format(P);
+    const bool fp8 = fmt == rc::kFmtFp8;
     if (fp8 && P.head_dim_k != 128) return RC_ERR_UNSUPPORTED;
     if (fp8 && (!P.k_scale || !P.v_scale)) return RC_ERR_ARG;
+    if (fmt == rc::kFmtFp4) {
+        const rc_status s = rc_host::check_fp4(P);
+        if (s != RC_OK) return s;
+        if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;
+    }
     rc::MQParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.pool_k = static_cast<const __nv_bfloat16*>(P.k);
@@ -90,12 +87,22 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
     p.lse = lse;
     p.k_scale = fp8 ? P.k_scale : nullptr;
     p.v_scale = fp8 ? P.v_scale : nullptr;
+    p.k_bscale = fmt == rc::kFmtFp4 ? P.k_bscale : nullptr;
+    p.v_bscale = fmt == rc::kFmtFp4 ? P.v_bscale : nullptr;
     const int G = desc->q_heads / P.kv_heads;
     bool ok = false;
     cudaError_t e = cudaSuccess;
     cudaStream_t st = (cudaStream_t)stream;
-    if (P.head_dim_k == 128) e = dispatch<128>(G, p, fp8, batch, max_q, P.kv_heads, st, &ok);
-    else if (P.head_dim_k == 64) e = dispatch<64>(G, p, false, batch, max_q, P.kv_heads, st, &ok);
+    if (fmt == rc::kFmtFp4) {
+        e = P.head_dim_k == 128 ? dispatch<128, rc::kFmtFp4>(G, p, batch, max_q, P.kv_heads, st, &ok)
+                                : dispatch<64, rc::kFmtFp4>(G, p, batch, max_q, P.kv_heads, st, &ok);
+    } else if (fp8) {
+        e = dispatch<128, rc::kFmtFp8>(G, p, batch, max_q, P.kv_heads, st, &ok);
+    } else if (P.head_dim_k == 128) {
+        e = dispatch<128, rc::kFmtBf16>(G, p, batch, max_q, P.kv_heads, st, &ok);
+    } else if (P.head_dim_k == 64) {
+        e = dispatch<64, rc::kFmtBf16>(G, p, batch, max_q, P.kv_heads, st, &ok);
+    }
     if (!ok) return RC_ERR_UNSUPPORTED;
     return rc_host::launch_status(e);
 }

@@ -38,6 +38,14 @@
 // tile's 64 K and 64 V scales; the softmax scales S by the K scales and folds
 // the V scales into P.  The ring has 4 stages (the scales take the room of
 // the fifth).
+//
+// 4-bit pool (E2M1 codes, one scale byte per 16 of them): as the FP8 pool, but
+// code times scale is itself an f16 value, so the producers store the pool's
+// exact values and the softmax is the bf16 pool's, with P in f16.
+//
+// Cross attention (kCross): extend without the causal edge, every token of
+// row z seeing all of the row's keys; with few rows of long keys the keys are
+// split over seg_chunks CTAs that leave partials, as the cascade does.
 #pragma once
 
 #include "mq_attn.cuh"
@@ -51,19 +59,22 @@ constexpr int ROWS = QT * TM;  // query rows per CTA
 constexpr int TN = 64;         // keys per tile
 constexpr int NS_BF16 = 5;     // K/V stages
 constexpr int NS_FP8 = 4;
+constexpr int NS_FP4 = 5;
 constexpr int NP = 2;          // producer warps (a third one measured no faster)
 constexpr int MMA_WARP = 8 + NP;
 constexpr int THREADS = 32 * (MMA_WARP + 1);
 constexpr uint32_t kWaitIter = 1u << 24;
-template <bool FP8>
-__host__ __device__ constexpr int stages() { return FP8 ? NS_FP8 : NS_BF16; }
-template <bool FP8>
-__host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FP8>() + 4 + 4 + 2; }
+template <int FMT>
+__host__ __device__ constexpr int stages() {
+    return FMT == rc::kFmtFp8 ? NS_FP8 : FMT == rc::kFmtFp4 ? NS_FP4 : NS_BF16;
+}
+template <int FMT>
+__host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FMT>() + 4 + 4 + 2; }
 
-template <int D, bool FP8 = false>
+template <int D, int FMT = rc::kFmtBf16>
 __host__ __device__ constexpr int smem_bytes() {
-    return QT * TM * D * 2 + stages<FP8>() * 2 * TN * D * 2 + (FP8 ? stages<FP8>() * 2 * TN * 4 : 0) +
-           n_bars<FP8>() * 8 + 16;
+    return QT * TM * D * 2 + stages<FMT>() * 2 * TN * D * 2 +
+           (FMT == rc::kFmtFp8 ? stages<FMT>() * 2 * TN * 4 : 0) + n_bars<FMT>() * 8 + 16;
 }
 
 // The cascade path reads FP8 pools too.
@@ -75,17 +86,19 @@ using tc::ffma2;
 using tc::max3;
 using tc::mbar_arrive;
 
-template <int D, int G, rc::MQMode MODE, bool FP8 = false>
+template <int D, int G, rc::MQMode MODE, int FMT = rc::kFmtBf16>
 __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams p) {
+    constexpr bool FP8 = FMT == rc::kFmtFp8, FP4 = FMT == rc::kFmtFp4;
+    constexpr bool F16 = FP8 || FP4;             // operands in f16, widened from codes
     static_assert(!FP8 || D == 128, "FP8 pools: head_dim 128");
-    constexpr int NS = stages<FP8>();
-    constexpr int kBars = n_bars<FP8>();
+    constexpr int NS = stages<FMT>();
+    constexpr int kBars = n_bars<FMT>();
     constexpr int CH = D / 8;
     constexpr int TPC = ROWS / G;               // tokens (or requests) per CTA
     constexpr int KV_BYTES = TN * D * 2;
     constexpr uint32_t SB = CH * 128;            // bytes between 8-row groups of Q/K/V tiles
-    constexpr uint32_t idS = FP8 ? tc::idesc_f16(TM, TN, false) : tc::idesc_bf16(TM, TN, false);
-    constexpr uint32_t idPV = FP8 ? tc::idesc_f16(TM, D, true) : tc::idesc_bf16(TM, D, true);
+    constexpr uint32_t idS = F16 ? tc::idesc_f16(TM, TN, false) : tc::idesc_bf16(TM, TN, false);
+    constexpr uint32_t idPV = F16 ? tc::idesc_f16(TM, D, true) : tc::idesc_bf16(TM, D, true);
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* sQ = smem;                                  // [QT][128 rows][D]
     unsigned char* sKV = sQ + QT * TM * D * 2;                 // [NS][K, V]
@@ -199,6 +212,40 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
         }
         keys = p.table + row0;
         key_count = prefix + min(n_rows_tok, tok0 + TPC);
+    } else if constexpr (MODE == rc::MQMode::kCross) {
+        const int b = z / p.seg_chunks;
+        chunk = z % p.seg_chunks;
+        qo0 = p.qo_indptr[b];
+        n_rows_tok = p.qo_indptr[b + 1] - qo0;
+        // more tokens than the caller's bounds (they size the grid and the
+        // partials): none of the row's is computed
+        if (n_rows_tok > p.max_q || qo0 < 0 || (int64_t)qo0 + n_rows_tok > p.max_rows) {
+            if (tid == 0) rc::flag_error(p.err, rc::kErrBadSlot);
+            return;
+        }
+        if (tok0 >= n_rows_tok) return;
+        const int64_t row0 = p.start[b];
+        int L = p.len[b];
+        if (row0 < 0 || L < 0 || row0 + L > p.table_len || L > p.max_len) {  // not read: as an empty row
+            if (tid == 0) rc::flag_error(p.err, rc::kErrBadSlot);
+            L = 0;
+        }
+        const int k0 = chunk * p.seg_chunk;
+        keys = p.table + row0 + k0;
+        key_count = min(L - k0, p.seg_chunk);
+        if (key_count <= 0) {  // nothing to attend to: a zero output, or an empty partial
+            for (int i = tid; i < min(n_rows_tok - tok0, TPC) * G; i += THREADS) {
+                const int64_t r = (int64_t)(qo0 + tok0 + i / G) * p.q_heads + kvh * G + i % G;
+                if (p.seg_chunks > 1) {
+                    p.part_lse[r * p.seg_chunks + chunk] = -INFINITY;
+                } else {
+                    for (int c = 0; c < CH; ++c)
+                        reinterpret_cast<uint4*>(p.out + r * D)[c] = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[r] = -INFINITY;
+                }
+            }
+            return;
+        }
     } else {
         const int seg = c_seg;
         chunk = c_chunk;
@@ -270,11 +317,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
             const int tk = tok0 + qr / G;
             const int h = kvh * G + (qr % G);
             qok[i] = tk < n_rows_tok;
-            if constexpr (MODE == rc::MQMode::kExtend) qrow[i] = (int64_t)(qo0 + tk) * p.q_heads + h;
+            if constexpr (MODE != rc::MQMode::kCascade) qrow[i] = (int64_t)(qo0 + tk) * p.q_heads + h;
             else qrow[i] = qok[i] ? (int64_t)__ldg(p.seg_rows + qo0 + tk) * p.q_heads + h : 0;
             if (!qok[i]) qrow[i] = 0;
         }
-        if constexpr (FP8) {  // f16 operand: load, convert, store
+        if constexpr (F16) {  // f16 operand: load, convert, store
             uint4 qv[CH];
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -417,6 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
                     const float2 e = make_float2(ex2(x.x), ex2(x.y));
                     ls[i & 3] = fadd2(ls[i & 3], e);
                     if constexpr (FP8) pk[i] = rc::pack_f16(e.x * tsc[TN + 2 * i], e.y * tsc[TN + 2 * i + 1]);
+                    else if constexpr (FP4) pk[i] = rc::pack_f16(e.x, e.y);
                     else pk[i] = rc::pack_bf16(e.x, e.y);
                 }
                 // P (bf16) over the first half of this S buffer: the A operand of P.V
@@ -485,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
                     const int tk = tok0 + rc_ / G;
                     const int hh = kvh * G + (rc_ % G);
                     if (!ok || tk >= n_rows_tok) continue;
-                    if constexpr (MODE == rc::MQMode::kExtend) {
+                    if (MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1)) {
                         uint2 w;
                         w.x = rc::pack_bf16(f.x, f.y);
                         w.y = rc::pack_bf16(f.z, f.w);
@@ -501,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
             }
             if (ok && row_valid) {
                 const int h = kvh * G + (row % G);
-                if constexpr (MODE == rc::MQMode::kExtend) {
+                if (MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1)) {
                     if (p.lse) p.lse[(int64_t)(qo0 + r_tok) * p.q_heads + h] = lse2 * rc::kLn2;
                 } else {
                     p.part_lse[((int64_t)(qo0 + r_tok) * p.q_heads + h) * p.seg_chunks + chunk] = lse2;
@@ -592,32 +640,85 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
                 }
                 tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
                 mbar_arrive(&kv_full[s]);
-                sl[0] = sl_next[0];
-                sl[1] = sl_next[1];
-                continue;
             }
+            if constexpr (FP4) {
+                // 16 bytes (32 codes) and their two block scales per lane: four
+                // lanes hold a 64-byte row, eight keys an instruction (D = 64:
+                // two lanes a row, sixteen keys).  The tile's K and V loads are
+                // all in flight together; every value is exact in f16.
+                constexpr int LPR = D / 32;          // lanes per row
+                constexpr int KPI = 32 / LPR;        // keys per instruction
+                constexpr int IT = TN / KPI;
+                const int krow = lane & (KPI - 1), cq = lane / KPI;
+                uint4 w4[2][IT];
+                uint32_t sc4[2][IT];
 #pragma unroll
-            for (int kg = 0; kg < TN / 8; ++kg) {
-                const int key = kg * 8 + klo;
-                int slot = __shfl_sync(0xffffffffu, sl[kg >> 2], (kg & 3) * 8 + klo);
-                uint32_t bytes = 16;
-                if (t * TN + key >= key_count) { slot = 0; bytes = 0; }
-                else if (slot < 0 || (int64_t)slot >= p.n_slots) {
-                    rc::flag_error(p.err, rc::kErrBadSlot);
-                    slot = 0;
-                    bytes = 0;
+                for (int i = 0; i < IT; ++i) {
+                    const int key = i * KPI + krow;
+                    int slot = __shfl_sync(0xffffffffu, sl[i * KPI >> 5], key & 31);
+                    bool live = t * TN + key < key_count;
+                    if (live && (slot < 0 || (int64_t)slot >= p.n_slots)) {
+                        rc::flag_error(p.err, rc::kErrBadSlot);
+                        live = false;
+                    }
+                    const int64_t row = (int64_t)(live ? slot : 0) * p.kv_heads + kvh;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const unsigned char* src = reinterpret_cast<const unsigned char*>(m ? p.pool_v : p.pool_k);
+                        const uint8_t* ssrc = m ? p.v_bscale : p.k_bscale;
+                        w4[m][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + row * (D / 2)) + cq)
+                                        : make_uint4(0, 0, 0, 0);
+                        sc4[m][i] = live ? __ldg(reinterpret_cast<const uint16_t*>(ssrc + row * (D / 16)) + cq) : 0u;
+                    }
                 }
-                // chunks c = 4 cg + csub: 512 bytes apart in the stage, 64 in the row
-                const int64_t base = ((int64_t)slot * p.kv_heads + kvh) * D + csub * 8;
-                const uint32_t off = tc::cm_offset(key, csub, CH);
-                rc::cp_async16_run<512, 64>(rc::smem_u32(sK) + off, p.pool_k + base, bytes, pol,
-                                            std::make_integer_sequence<int, CH / 4>{});
-                rc::cp_async16_run<512, 64>(rc::smem_u32(sV) + off, p.pool_v + base, bytes, pol,
-                                            std::make_integer_sequence<int, CH / 4>{});
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    unsigned char* dst = m ? sV : sK;
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        const int key = i * KPI + krow;
+                        const uint32_t s0 = rc::scale_pair<0, 0>(sc4[m][i]), s1 = rc::scale_pair<1, 1>(sc4[m][i]);
+                        const uint32_t x[4] = {w4[m][i].x, w4[m][i].y, w4[m][i].z, w4[m][i].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {  // 8 codes: f16 chunk 4 cq + c
+                            uint4 f;
+                            rc::e2m1x8_to_f16x8(x[c], f.x, f.y, f.z, f.w);
+                            const uint32_t sc = c < 2 ? s0 : s1;
+                            f.x = rc::mul_f16x2(f.x, sc);
+                            f.y = rc::mul_f16x2(f.y, sc);
+                            f.z = rc::mul_f16x2(f.z, sc);
+                            f.w = rc::mul_f16x2(f.w, sc);
+                            *reinterpret_cast<uint4*>(dst + tc::cm_offset(key, 4 * cq + c, CH)) = f;
+                        }
+                    }
+                }
+                tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
+                mbar_arrive(&kv_full[s]);
             }
-            // each lane arrives on the stage's barrier when its copies have
-            // landed; the warp goes on to the next tile at once
-            tc::cp_async_mbar_arrive(&kv_full[s]);
+            if constexpr (!F16) {
+#pragma unroll
+                for (int kg = 0; kg < TN / 8; ++kg) {
+                    const int key = kg * 8 + klo;
+                    int slot = __shfl_sync(0xffffffffu, sl[kg >> 2], (kg & 3) * 8 + klo);
+                    uint32_t bytes = 16;
+                    if (t * TN + key >= key_count) { slot = 0; bytes = 0; }
+                    else if (slot < 0 || (int64_t)slot >= p.n_slots) {
+                        rc::flag_error(p.err, rc::kErrBadSlot);
+                        slot = 0;
+                        bytes = 0;
+                    }
+                    // chunks c = 4 cg + csub: 512 bytes apart in the stage, 64 in the row
+                    const int64_t base = ((int64_t)slot * p.kv_heads + kvh) * D + csub * 8;
+                    const uint32_t off = tc::cm_offset(key, csub, CH);
+                    rc::cp_async16_run<512, 64>(rc::smem_u32(sK) + off, p.pool_k + base, bytes, pol,
+                                                std::make_integer_sequence<int, CH / 4>{});
+                    rc::cp_async16_run<512, 64>(rc::smem_u32(sV) + off, p.pool_v + base, bytes, pol,
+                                                std::make_integer_sequence<int, CH / 4>{});
+                }
+                // each lane arrives on the stage's barrier when its copies have
+                // landed; the warp goes on to the next tile at once
+                tc::cp_async_mbar_arrive(&kv_full[s]);
+            }
             sl[0] = sl_next[0];
             sl[1] = sl_next[1];
         }

@@ -17,6 +17,11 @@ namespace rc {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// How a pool's rows are held (a template argument of the kernels).
+constexpr int kFmtBf16 = 0;
+constexpr int kFmtFp8 = 1;  // E4M3 codes, one fp32 scale per row
+constexpr int kFmtFp4 = 2;  // E2M1 codes, one scale byte per 16 of them
+
 // Error bits OR-ed into the caller's device error word.
 constexpr int32_t kErrBadSlot = 1;
 constexpr int32_t kErrTimeout = 2;
@@ -161,6 +166,23 @@ RC_DEV void e4m3x4_to_f16x4(uint32_t four_codes, uint32_t& lo, uint32_t& hi) {
         : "r"(four_codes));
 }
 
+// Eight E2M1 codes (one word, low nibble first) to four f16 pairs, exact.  The
+// instruction runs at the rate of a byte permute and takes any byte of the
+// word, so a word costs four of them and nothing else.
+RC_DEV void e2m1x8_to_f16x8(uint32_t w, uint32_t& o0, uint32_t& o1, uint32_t& o2, uint32_t& o3) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+        : "=r"(o0), "=r"(o1), "=r"(o2), "=r"(o3)
+        : "r"(w));
+}
+// Product of f16 pairs, each rounded to nearest.  An E2M1 code times a block
+// scale has at most six significant bits and lies in f16's range: exact.
+RC_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // A bf16 pair to an f16 pair (exact while |x| is within f16's range).
 RC_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
     return pack_f16(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -171,6 +193,14 @@ RC_DEV uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
+}
+
+// Block scales of a 4-bit pool (an f16's bits 14..7) as f16 pairs: the bytes
+// `lo` and `hi` (0..3) of `bytes` into the low and the high half.  A half is
+// its byte at bits 14..7, so the pair is (byte << 8) shifted right by one.
+template <int LO, int HI>
+RC_DEV uint32_t scale_pair(uint32_t bytes) {
+    return prmt(bytes, 0u, 0x0404u | (LO << 4) | (HI << 12)) >> 1;
 }
 
 RC_DEV uint32_t pack_bf16(float lo, float hi) {
@@ -193,6 +223,23 @@ RC_DEV uint32_t swz(int r, int c) {
 // Host-side launch helpers.
 namespace rc_host {
 int sm_count();
+// The pool's kFmt* as its descriptor says.
+inline int pool_format(const rc_pool_desc& p) {
+    return p.kv_fp8 == 0 ? rc::kFmtBf16 : p.kv_fp8 == RC_KV_FP4 ? rc::kFmtFp4 : rc::kFmtFp8;
+}
+// Head layout and arrays of a 4-bit pool.
+inline rc_status check_fp4(const rc_pool_desc& p) {
+    if (p.mla || p.head_dim_k != p.head_dim_v || (p.head_dim_k != 128 && p.head_dim_k != 64))
+        return RC_ERR_UNSUPPORTED;
+    if (!p.k || !p.v || !p.k_bscale || !p.v_bscale) return RC_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) |
+         reinterpret_cast<uintptr_t>(p.k_bscale) | reinterpret_cast<uintptr_t>(p.v_bscale)) & 15)
+        return RC_ERR_ARG;
+    return RC_OK;
+}
+// kv_store on a 4-bit pool, kv_store_rope.cu
+rc_status store_fp4(const rc_pool_desc* pool, const int32_t* slots, const void* k_new, const void* v_new, int32_t n,
+                    int32_t* table, const int32_t* table_pos, cudaStream_t st);
 // latent (MLA) decode, attn_decode_mla.cu
 size_t mla_workspace(int32_t batch, int32_t q_heads, int32_t max_len);
 rc_status mla_decode(const rc_attn_desc* desc, const void* q, const rc_kv_table* kv, int32_t batch, void* out,

@@ -97,6 +97,8 @@ extern "C" rc_status kv_store(const rc_pool_desc* pool, const int32_t* slots, co
     if (n == 0) return RC_OK;
     if (!slots || !k_new) return RC_ERR_ARG;
     if ((table == nullptr) != (table_pos == nullptr)) return RC_ERR_ARG;
+    if (rc_host::pool_format(*pool) == rc::kFmtFp4)
+        return rc_host::store_fp4(pool, slots, k_new, v_new, n, table, table_pos, (cudaStream_t)stream);
     if (pool->kv_fp8) {
         if (pool->mla || pool->head_dim_k != 128 || pool->head_dim_v != 128) return RC_ERR_UNSUPPORTED;
         if (!pool->v || !v_new || !pool->k_scale || !pool->v_scale) return RC_ERR_ARG;

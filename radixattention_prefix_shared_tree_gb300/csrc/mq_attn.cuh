@@ -8,7 +8,7 @@
 
 namespace rc {
 
-enum class MQMode { kExtend, kCascade };
+enum class MQMode { kExtend, kCascade, kCross };
 
 struct MQParams {
     const __nv_bfloat16* q;
@@ -47,6 +47,14 @@ struct MQParams {
     // FP8 pool: pool_k / pool_v hold E4M3 codes and these the per-row scales
     const float* k_scale;  // [n_slots][kv_heads]
     const float* v_scale;
+    // 4-bit pool: pool_k / pool_v hold E2M1 codes and these the block scales
+    const uint8_t* k_bscale;  // [n_slots][kv_heads][D / 16]
+    const uint8_t* v_bscale;
+    // cross: the caller's bounds on a row's tokens, all tokens and a row's keys
+    // (seg_chunk keys a CTA, seg_chunks CTAs a row: grid z = row * seg_chunks + chunk)
+    int32_t max_q;
+    int32_t max_len;
+    int64_t max_rows;
 };
 
 }  // namespace rc
