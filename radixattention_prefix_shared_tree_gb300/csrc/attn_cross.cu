@@ -24,9 +24,9 @@ using namespace rc_dec;
 constexpr int kFewColumns = 8;   // the n = 8 side of the table pass's products
 
 struct CrossPlan {
-    bool few = false;
+    bool few = false, runs = false;  // runs: the 4-bit table pass over equal runs of keys
     int chunk = 0, n_chunks = 1;
-    size_t part_o = 0, part_lse = 0, total = 0;
+    size_t part_o = 0, part_lse = 0, row_runs = 0, total = 0;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -42,8 +42,7 @@ rc_status plan_cross(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_
     int64_t splits = 1, step;
     if (pl->few) {  // as attn_decode: one wave of warps, at least 64 keys each
         const int64_t base = (int64_t)batch * hkv;
-        const int64_t warps = rc_host::pool_format(P) == rc::kFmtFp4 ? fp4::kWarps : kWarpsPerCta;
-        if (base > 0 && base < 8 * sms) splits = warps * sms / base;
+        if (base > 0 && base < 8 * sms) splits = kWarpsPerCta * sms / base;
         step = kDecKeys;
     } else {  // one CTA per SM, at least 256 keys each
         const int64_t grid = ((cols + rc_tc2::ROWS - 1) / rc_tc2::ROWS) * hkv * batch;
@@ -57,12 +56,22 @@ rc_status plan_cross(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_
     if (chunk > 0x7fffffc0) return RC_ERR_ARG;
     pl->chunk = (int)chunk;
     pl->n_chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
-    if (pl->n_chunks > 1) {
+    pl->runs = pl->few && rc_host::pool_format(P) == rc::kFmtFp4 && !fp4::whole_rows(batch, hkv, max_len, sms);
+    if (pl->few && rc_host::pool_format(P) == rc::kFmtFp4) {
+        pl->chunk = max_len > 0 ? max_len : 1;
+        pl->n_chunks = pl->runs ? fp4::groups(batch, hkv, max_len, sms) : 1;
+    }
+    if (pl->runs) {
+        const size_t parts = ((size_t)pl->n_chunks + batch) * hkv * kFewColumns;
+        pl->part_o = align256(parts * P.head_dim_v * sizeof(float));
+        pl->part_lse = align256(parts * sizeof(float));
+        pl->row_runs = align256((size_t)batch * 2 * sizeof(int32_t));
+    } else if (pl->n_chunks > 1) {
         const size_t rows = (size_t)batch * max_q * d->q_heads * pl->n_chunks;
         pl->part_o = align256(rows * P.head_dim_v * sizeof(float));
         pl->part_lse = align256(rows * sizeof(float));
     }
-    pl->total = pl->part_o + pl->part_lse;
+    pl->total = pl->part_o + pl->part_lse + pl->row_runs;
     return RC_OK;
 }
 
@@ -130,11 +139,11 @@ __global__ void __launch_bounds__(256) cross_merge_kernel(const float* __restric
     }
 }
 
-template <auto Kernel, int WARPS>
+template <auto Kernel, int WARPS, bool RUNS = false>
 cudaError_t launch_few(const DecParams& p, int smem, int batch, cudaStream_t st) {
     cudaError_t e = rc_host::ensure_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
-    const int n_items = batch * p.kv_heads * p.n_chunks;
+    const int n_items = RUNS ? p.kv_heads * p.n_chunks : batch * p.kv_heads * p.n_chunks;
     Kernel<<<(n_items + WARPS - 1) / WARPS, 32 * WARPS, smem, st>>>(p, n_items);
     return cudaGetLastError();
 }
@@ -142,8 +151,8 @@ cudaError_t launch_few(const DecParams& p, int smem, int batch, cudaStream_t st)
 template <int D, int FMT, bool FUSED>
 cudaError_t few(const DecParams& p, int batch, cudaStream_t st) {
     if constexpr (FMT == rc::kFmtFp4)
-        return launch_few<decode_fp4_kernel<D, kFewColumns, FUSED, true>, fp4::kWarps>(p, fp4::smem_bytes<D>(), batch,
-                                                                                       st);
+        return launch_few<decode_fp4_kernel<D, kFewColumns, FUSED, true>, fp4::kWarps, !FUSED>(
+            p, fp4::smem_bytes<D>(), batch, st);
     else
         return launch_few<decode_split_kernel<D, kFewColumns, FUSED, FMT == rc::kFmtFp8, true>, kWarpsPerCta>(
             p, dec_smem_bytes<D, FMT == rc::kFmtFp8>(), batch, st);
@@ -174,7 +183,7 @@ template <int D, int FMT>
 cudaError_t run(const CrossPlan& pl, int G, const DecParams& dp, const rc::MQParams& mp, int batch, int max_q,
                 cudaStream_t st) {
     if (!pl.few) return many<D, FMT>(G, mp, batch, max_q, st);
-    return pl.n_chunks == 1 ? few<D, FMT, true>(dp, batch, st) : few<D, FMT, false>(dp, batch, st);
+    return pl.n_chunks == 1 && !pl.runs ? few<D, FMT, true>(dp, batch, st) : few<D, FMT, false>(dp, batch, st);
 }
 
 }  // namespace
@@ -210,6 +219,7 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     const int64_t max_rows = (int64_t)batch * max_q;
     // grid limits: blocks in x for the table pass and the merge, z for the many-row kernel
     if ((int64_t)batch * P.kv_heads * pl.n_chunks > 0x7fffffff || max_rows > 0x7fffffff) return RC_ERR_ARG;
+    if (pl.runs && desc->q_heads > 65535) return RC_ERR_UNSUPPORTED;
     if (!pl.few && ((int64_t)batch * pl.n_chunks > 65535 || P.kv_heads > 65535)) return RC_ERR_UNSUPPORTED;
     unsigned char* w = static_cast<unsigned char*>(ws);
     float* part_o = reinterpret_cast<float*>(w);
@@ -247,6 +257,8 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     dp.max_len = mp.max_len = kv->max_len;
     dp.max_rows = mp.max_rows = max_rows;
     dp.group = G;
+    dp.batch = batch;
+    dp.row_runs = reinterpret_cast<int32_t*>(w + pl.part_o + pl.part_lse);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     const bool wide = P.head_dim_k == 128;
@@ -259,7 +271,7 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
         e = wide ? run<128, rc::kFmtBf16>(pl, G, dp, mp, batch, max_q, st)
                  : run<64, rc::kFmtBf16>(pl, G, dp, mp, batch, max_q, st);
     if (e != cudaSuccess) return RC_ERR_CUDA;
-    if (pl.n_chunks == 1) return RC_OK;
+    if (pl.n_chunks == 1 && !pl.runs) return RC_OK;
     // the merge starts as the pass's CTAs leave and waits for its end inside
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)max_rows);
@@ -270,6 +282,12 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (pl.runs) {
+        cfg.gridDim = dim3((unsigned)max_rows, desc->q_heads);
+        cfg.blockDim = dim3(32 * fp4::kMergeWarps);
+        e = cudaLaunchKernelEx(&cfg, wide ? merge_runs_kernel<128, true> : merge_runs_kernel<64, true>, dp);
+        return rc_host::launch_status(e);
+    }
     e = cudaLaunchKernelEx(&cfg, wide ? cross_merge_kernel<128> : cross_merge_kernel<64>, (const float*)part_o,
                            (const float*)part_lse, pl.n_chunks, qo_indptr, max_q, max_rows, desc->q_heads,
                            static_cast<__nv_bfloat16*>(out), lse, (const int32_t*)P.err);

@@ -127,7 +127,7 @@ struct DecodePlan {
     int chunk = 0, n_chunks = 0;        // table part: keys per CTA, CTAs per row
     int seg_chunk = 0, seg_chunks = 0;  // cascade: keys per CTA, CTAs per segment
     bool fused = false;                 // one CTA per (row, KV head): no merge pass
-    size_t tail_o = 0, tail_lse = 0, seg_o = 0, seg_lse = 0, total = 0;
+    size_t tail_o = 0, tail_lse = 0, row_runs = 0, seg_o = 0, seg_lse = 0, total = 0;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -145,10 +145,10 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
     // tiles, about 2.5 us per 16 keys when the gather saturates HBM, so the
     // wave's longest item sets the call), down to 64 keys per chunk.
     const int64_t base = (int64_t)batch * hkv;
-    const int64_t warps = rc_host::pool_format(d->pool) == rc::kFmtFp4 ? fp4::kWarps : kWarpsPerCta;
+    const bool is_fp4 = rc_host::pool_format(d->pool) == rc::kFmtFp4;
     int64_t splits = 1;
     if (base < 8 * sms) {
-        splits = base > 0 ? (warps * sms) / base : 1;
+        splits = base > 0 ? (kWarpsPerCta * sms) / base : 1;
         const int64_t max_splits = max_len > 0 ? (max_len + kDecKeys - 1) / kDecKeys : 1;
         if (splits > max_splits) splits = max_splits;
         if (splits < 1) splits = 1;
@@ -158,6 +158,11 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
     pl->chunk = (int)chunk;
     pl->n_chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
     pl->fused = pl->n_chunks == 1;
+    if (is_fp4) {  // whole rows, or equal runs of the batch's keys (n_chunks of them)
+        pl->fused = fp4::whole_rows(batch, hkv, max_len, sms);
+        pl->chunk = max_len > 0 ? max_len : 1;
+        pl->n_chunks = pl->fused ? 1 : fp4::groups(batch, hkv, max_len, sms);
+    }
     // Cascade part: split each segment's keys so that the grid fills the SMs
     // once (one CTA per SM: a second, partial wave would double the time),
     // and in any case so that no CTA takes more than about kSegKeys keys: a
@@ -186,10 +191,16 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
     const size_t rows = (size_t)batch * d->q_heads;
     pl->tail_o = pl->fused ? 0 : align256(rows * pl->n_chunks * dv * sizeof(float));
     pl->tail_lse = pl->fused ? 0 : align256(rows * pl->n_chunks * sizeof(float));
+    if (is_fp4 && !pl->fused) {
+        const size_t parts = ((size_t)pl->n_chunks + batch) * d->q_heads;
+        pl->tail_o = align256(parts * dv * sizeof(float));
+        pl->tail_lse = align256(parts * sizeof(float));
+        pl->row_runs = align256((size_t)batch * 2 * sizeof(int32_t));
+    }
     const size_t srows = casc && casc->n_seg > 0 ? (size_t)casc->total_seg_rows * d->q_heads * pl->seg_chunks : 0;
     pl->seg_o = align256(srows * dv * sizeof(float));
     pl->seg_lse = align256(srows * sizeof(float));
-    pl->total = pl->tail_o + pl->tail_lse + pl->seg_o + pl->seg_lse;
+    pl->total = pl->tail_o + pl->tail_lse + pl->row_runs + pl->seg_o + pl->seg_lse;
     if (pl->total == 0) pl->total = 256;
     return RC_OK;
 }
@@ -197,11 +208,12 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
 // after_cascade: launched as the programmatic dependent of the cascade kernel
 // just queued on the stream, so that its CTAs start on SMs the cascade leaves
 // free and as cascade CTAs finish, instead of after the whole cascade grid.
-template <auto Kernel, int WARPS>
+// RUNS: a warp per (run, KV head) instead of (row, KV head, chunk).
+template <auto Kernel, int WARPS, bool RUNS = false>
 cudaError_t launch_table(const DecParams& p, int smem, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
     cudaError_t e = rc_host::ensure_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
-    const int n_items = batch * kv_heads * p.n_chunks;
+    const int n_items = RUNS ? kv_heads * p.n_chunks : batch * kv_heads * p.n_chunks;
     const int grid = (n_items + WARPS - 1) / WARPS;
     if (!after_cascade) {
         Kernel<<<grid, 32 * WARPS, smem, st>>>(p, n_items);
@@ -223,7 +235,7 @@ cudaError_t launch_table(const DecParams& p, int smem, int batch, int kv_heads, 
 template <int D, int G, bool FUSED, int FMT>
 cudaError_t launch_split(const DecParams& p, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
     if constexpr (FMT == rc::kFmtFp4)
-        return launch_table<decode_fp4_kernel<D, G, FUSED, false>, fp4::kWarps>(p, fp4::smem_bytes<D>(), batch,
+        return launch_table<decode_fp4_kernel<D, G, FUSED, false>, fp4::kWarps, !FUSED>(p, fp4::smem_bytes<D>(), batch,
                                                                                kv_heads, st, after_cascade);
     else
         return launch_table<decode_split_kernel<D, G, FUSED, FMT == rc::kFmtFp8>, kWarpsPerCta>(
@@ -357,8 +369,9 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     }
     const int G = desc->q_heads / P.kv_heads;
     unsigned char* w = static_cast<unsigned char*>(ws);
-    float* seg_o = reinterpret_cast<float*>(w + pl.tail_o + pl.tail_lse);
-    float* seg_lse = reinterpret_cast<float*>(w + pl.tail_o + pl.tail_lse + pl.seg_o);
+    unsigned char* ws_seg = w + pl.tail_o + pl.tail_lse + pl.row_runs;
+    float* seg_o = reinterpret_cast<float*>(ws_seg);
+    float* seg_lse = reinterpret_cast<float*>(ws_seg + pl.seg_o);
     DecParams dp{};
     dp.q = static_cast<const __nv_bfloat16*>(q);
     dp.pool_k = static_cast<const __nv_bfloat16*>(P.k);
@@ -390,6 +403,9 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     dp.k_bscale = fmt == rc::kFmtFp4 ? P.k_bscale : nullptr;
     dp.v_bscale = fmt == rc::kFmtFp4 ? P.v_bscale : nullptr;
     dp.group = G;
+    dp.batch = batch;
+    dp.max_len = kv->max_len;
+    dp.row_runs = reinterpret_cast<int32_t*>(w + pl.tail_o + pl.tail_lse);
     rc::MQParams mp{};
     mp.q = dp.q;
     mp.pool_k = dp.pool_k;
@@ -439,14 +455,16 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     // inside), so its CTAs start as the split pass's leave
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(nbh);
-    cfg.blockDim = dim3(32);
+    cfg.blockDim = dim3(fmt == rc::kFmtFp4 ? 32 * fp4::kMergeWarps : 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (D == 128)
+    if (fmt == rc::kFmtFp4)
+        e = cudaLaunchKernelEx(&cfg, D == 128 ? merge_runs_kernel<128, false> : merge_runs_kernel<64, false>, dp);
+    else if (D == 128)
         e = cudaLaunchKernelEx(&cfg, merge_kernel<128>, (const float*)dp.part_o, (const float*)dp.part_lse,
                                dp.n_chunks, dp.chunk, dp.len, (const float*)seg_o, (const float*)seg_lse,
                                pl.seg_chunks, ri, rp, desc->q_heads, dp.start, dp.table_len, o, lse, P.err);

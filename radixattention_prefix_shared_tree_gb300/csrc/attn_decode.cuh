@@ -47,6 +47,10 @@ struct DecParams {
     // the caller's bounds on a row's tokens, all tokens and a row's keys
     const int32_t* qo_indptr;
     int32_t group;       // query heads per KV head
+    // 4-bit pool, split rows: n_chunks is the number of runs and part_o is
+    // [runs + batch][kv_heads][columns][D] (attn_decode_fp4.cuh)
+    int32_t batch;
+    int32_t* row_runs;   // [batch][2]: first and last run that touch the row
     int32_t max_q;
     int32_t max_len;
     int64_t max_rows;
@@ -105,6 +109,36 @@ RC_DEV Item decode_item(const DecParams& p, int it, int lane) {
     w.k0 = w.chunk * p.chunk;
     w.count = max(0, min(w.L - w.k0, p.chunk));
     return w;
+}
+
+// Row b's keys (and, CROSS, its tokens) as the 4-bit pool's passes and their
+// merge read them: L = 0 for a row that is not there, lies outside the table
+// or (CROSS) exceeds the caller's bounds or has no tokens; decode reads a row
+// longer than max_len up to it.
+struct RowKeys {
+    int64_t row0;
+    int L, qo0, ncol;
+    bool bad;
+};
+template <bool CROSS>
+RC_DEV RowKeys row_keys(const DecParams& p, int b) {
+    RowKeys r{0, 0, 0, 0, false};
+    if (b >= p.batch) return r;
+    r.row0 = __ldg(p.start + b);
+    r.L = __ldg(p.len + b);
+    r.bad = r.row0 < 0 || r.L < 0 || r.row0 + r.L > p.table_len || r.L > p.max_len;
+    if constexpr (CROSS) {
+        r.qo0 = __ldg(p.qo_indptr + b);
+        const int nq = __ldg(p.qo_indptr + b + 1) - r.qo0;
+        const bool bad_q = nq > p.max_q || r.qo0 < 0 || (int64_t)r.qo0 + nq > p.max_rows;
+        r.ncol = bad_q || nq < 0 ? 0 : nq * p.group;
+        if (r.bad || r.ncol == 0) r.L = 0;
+        r.bad = r.bad || bad_q;
+    } else if (r.bad) {
+        const bool too_long = r.row0 >= 0 && r.L > p.max_len && r.row0 + r.L <= p.table_len;
+        r.L = too_long ? p.max_len : 0;
+    }
+    return r;
 }
 
 // A split item without keys: decode leaves its partial unwritten (the merge

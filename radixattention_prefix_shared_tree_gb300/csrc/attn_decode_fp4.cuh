@@ -28,7 +28,8 @@ namespace rc_dec {
 namespace fp4 {
 
 constexpr int kKeys = 32;          // keys per tile: a lane's slot id each
-constexpr int kWarps = 16;         // per CTA
+constexpr int kWarps = 4;          // per CTA
+constexpr int kCtasPerSm = 4;      // 16 warps' rings and registers fill an SM
 constexpr int kStages = 3;
 
 template <int D>
@@ -41,6 +42,27 @@ template <int D>
 __host__ __device__ constexpr int warp_bytes() { return kStages * stage_bytes<D>(); }
 template <int D>
 __host__ __device__ constexpr int smem_bytes() { return kWarps * warp_bytes<D>(); }
+
+// How the split pass divides a batch: all rows' keys, 32 to a tile, laid end to
+// end and cut into equal runs of tiles, one run per group of kv_heads warps (a
+// warp per KV head).  Every warp then has the same work whatever the rows'
+// lengths, and a row has one partial per run that touches it.  Run g's part of
+// row b goes to partial slot g + b: runs and rows both only move forward, so
+// no two parts share a sum, and a row's slots are consecutive.
+// At most as many runs as fit the SMs at once, of at least kMinTiles tiles.
+constexpr int kMinTiles = 2;
+inline int groups(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t sms) {
+    const int64_t resident = (int64_t)kWarps * kCtasPerSm * sms / kv_heads;
+    const int64_t tiles = batch * ((max_len + kKeys - 1) / kKeys);
+    const int64_t most = (tiles + kMinTiles - 1) / kMinTiles;
+    const int64_t g = resident < most ? resident : most;
+    return (int)(g < 1 ? 1 : g);
+}
+// One warp per (row, KV head) and no merge: rows short enough, and enough of
+// them, that a warp each fills most of the SMs.
+inline bool whole_rows(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t sms) {
+    return 2 * batch * kv_heads >= (int64_t)kWarps * kCtasPerSm * sms && max_len <= 512;
+}
 
 // 4- or 8-byte asynchronous copy (block scales); src_bytes = 0 writes zeros.
 template <int N>
@@ -58,10 +80,14 @@ RC_DEV int v_row(int m) { return (m & 16) | ((m & 14) >> 1) | ((m & 1) << 3); }
 template <int D>
 RC_DEV int v_swz(int r) { return D == 128 ? (r & 2) : 0; }
 
+constexpr int kMergeWarps = 4;
+
 }  // namespace fp4
 
+// FUSED: one item per warp, result written (and the row's cascade partials
+// folded in) by its epilogue.  Otherwise the equal runs described above.
 template <int D, int NC, bool FUSED, bool CROSS>
-__global__ void __launch_bounds__(32 * fp4::kWarps, 1) decode_fp4_kernel(const DecParams p, int n_items) {
+__global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_kernel(const DecParams p, int n_items) {
     using namespace fp4;
     static_assert(D == 128 || D == 64, "head_dim");
     constexpr int KS = D / 16;                 // k-steps of S, m-tiles of O
@@ -80,68 +106,144 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, 1) decode_fp4_kernel(const D
         return;
     }
     unsigned char* wbase = smem + warp * warp_bytes<D>();
-    const Item w = decode_item<NC, FUSED, CROSS>(p, it, lane);
-    if (CROSS && w.ncol == 0) {
-        grid_dep_wait();
-        return;
+    Item w;
+    SegParts seg{0, 0};
+    int64_t first_row = 0;
+    // !FUSED: this warp's run of tiles [run, run_end), the row it stands in
+    // and the first tile of that row
+    int64_t run = 0, run_end = 1, row_tile = 0;
+    int group = 0, row_tiles = 0;
+    bool waited = false;
+    if constexpr (FUSED) {
+        w = decode_item<NC, FUSED, CROSS>(p, it, lane);
+        if (CROSS && w.ncol == 0) {
+            grid_dep_wait();
+            return;
+        }
+        if (!CROSS && p.req_seg_indptr) {
+            seg.e0 = p.req_seg_indptr[w.b];
+            seg.n_parts = (p.req_seg_indptr[w.b + 1] - seg.e0) * p.seg_chunks;
+        }
+        first_row = seg.row(p, lane);
+    } else {
+        w.kvh = it % p.kv_heads;
+        w.q_heads = p.q_heads;
+        w.group = p.group;
+        group = it / p.kv_heads;
+        int64_t tiles = 0;  // of the whole batch
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            RowKeys r = row_keys<CROSS>(p, b0 + lane);
+            if (r.bad && it == 0) rc::flag_error(p.err, rc::kErrBadSlot);
+            tiles += (r.L + kKeys - 1) / kKeys;
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, k);
+        int64_t runs = (tiles + kMinTiles - 1) / kMinTiles;
+        runs = runs < p.n_chunks ? runs : p.n_chunks;
+        if (group >= runs) {
+            grid_dep_wait();
+            return;
+        }
+        run = group * tiles / runs;
+        run_end = (group + 1) * tiles / runs;
+        w.b = -1;
+        for (int b0 = 0; w.b < 0 && b0 < p.batch; b0 += 32) {  // the row that holds tile `run`
+            const int n = (row_keys<CROSS>(p, b0 + lane).L + kKeys - 1) / kKeys;
+            int64_t incl = n;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
+                if (lane >= k) incl += v;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, run < row_tile + incl);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                w.b = b0 + src;
+                row_tile += __shfl_sync(0xffffffffu, incl - n, src);
+            } else {
+                row_tile += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
     }
-    if (!FUSED && w.count == 0) {
-        grid_dep_wait();
-        empty_partial<CROSS>(p, w, lane);
-        return;
+    const uint64_t pol = rc::l2_policy_evict_first();  // a request's own keys are read once per step
+    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.pool_k) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
+    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.pool_v) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
+    const uint8_t* ksc = p.k_bscale + (int64_t)w.kvh * SB;
+    const uint8_t* vsc = p.v_bscale + (int64_t)w.kvh * SB;
+    const uint32_t row_codes = (uint32_t)p.kv_heads * CB, row_scales = (uint32_t)p.kv_heads * SB;
+    const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);
+    // where this lane's copies of instruction 0 go; instruction i's are a
+    // constant further: RPI rows of K, and the same rows' places in V
+    const uint32_t kdst = rc::smem_u32(wbase) + lane * 16;
+    const int vr0 = v_row(lane / CPR);
+    const uint32_t vdst = rc::smem_u32(wbase) + kKeys * CB + vr0 * CB + ((lane % CPR) ^ v_swz<D>(vr0)) * 16;
+    const uint32_t sdst = rc::smem_u32(wbase) + 2 * kKeys * CB + lane * SB;
+
+    while (run < run_end && (FUSED || (w.b >= 0 && w.b < p.batch))) {
+    if constexpr (FUSED) {
+        run = run_end;
+    } else {  // the part of row w.b that lies in the run
+        const RowKeys r = row_keys<CROSS>(p, w.b);
+        row_tiles = (r.L + kKeys - 1) / kKeys;
+        const int64_t lo = run - row_tile;
+        if (lo >= row_tiles) {  // the run goes on in the next row
+            row_tile += row_tiles;
+            ++w.b;
+            continue;
+        }
+        const int64_t n = min((int64_t)row_tiles - lo, run_end - run);
+        w.row0 = r.row0;
+        w.ncol = CROSS ? r.ncol : NC;
+        w.qrow0 = CROSS ? (int64_t)r.qo0 * p.q_heads + w.kvh * p.group : (int64_t)w.b * p.q_heads + w.kvh * NC;
+        w.k0 = (int)lo * kKeys;
+        w.count = (int)min((int64_t)r.L - w.k0, n * kKeys);
+        if (lane == 0 && w.kvh == 0) {  // for the merge: the runs that touch the row
+            if (lo == 0) p.row_runs[2 * w.b] = group;
+            if (lo + n == row_tiles) p.row_runs[2 * w.b + 1] = group;
+        }
+        run += n;
     }
     const int count = w.count;
     const int32_t* keys = p.table + w.row0 + w.k0;
     const int n_tiles = (count + kKeys - 1) / kKeys;
-    SegParts seg{0, 0};
-    if (FUSED && !CROSS && p.req_seg_indptr) {
-        seg.e0 = p.req_seg_indptr[w.b];
-        seg.n_parts = (p.req_seg_indptr[w.b + 1] - seg.e0) * p.seg_chunks;
-    }
-    const int64_t first_row = seg.row(p, lane);
-
-    // Lane l holds the slot id of key l of a tile: -1 past the end and for an
-    // id outside the pool (flagged), whose row then reads as zeros.
+    // Lane l holds the slot id of key l of a tile, -1 past the end.  It is read
+    // one tile before its copies are issued and looked at only then, so the
+    // load's latency is never waited for.
     auto slot_of = [&](int t) -> int {
         const int key = t * kKeys + lane;
-        if (key >= count) return -1;
-        const int s = __ldg(keys + key);
-        if (s < 0 || (int64_t)s >= p.n_slots) {
-            rc::flag_error(p.err, rc::kErrBadSlot);
-            return -1;
-        }
-        return s;
+        return key < count ? __ldg(keys + key) : -1;
     };
-    const uint64_t pol = rc::l2_policy_evict_first();  // a request's own keys are read once per step
-    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.pool_k) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
-    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.pool_v) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
-    const int64_t row_stride = (int64_t)p.kv_heads * CB;
-    const uint32_t sbase = rc::smem_u32(wbase);
     auto issue = [&](int t, int slot) {
-        if (t < n_tiles) {
-            const uint32_t st = sbase + (t % kStages) * STAGE;
+        if (t >= n_tiles) return;
+        const uint32_t st = (t % kStages) * STAGE;
+        // an id outside the pool reads as a row of zeros (flagged)
+        const bool ok = (uint32_t)slot < n_slots;
+        if (!ok && t * kKeys + lane < count) rc::flag_error(p.err, rc::kErrBadSlot);
+        const int id = ok ? slot : -1;
 #pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-                const int r = i * RPI + lane / CPR;
-                const int s = __shfl_sync(0xffffffffu, slot, r);
-                const int64_t off = (int64_t)(s < 0 ? 0 : s) * row_stride;
-                const uint32_t bytes = s < 0 ? 0u : 16u;
-                const int vr = v_row(r);
-                rc::cp_async16(st + r * CB + (lane % CPR) * 16, kc + off, bytes, pol);
-                rc::cp_async16(st + kKeys * CB + vr * CB + ((lane % CPR) ^ v_swz<D>(vr)) * 16, vc + off, bytes, pol);
-            }
-            const int64_t soff = ((int64_t)(slot < 0 ? 0 : slot) * p.kv_heads + w.kvh) * SB;
-            const uint32_t sb = slot < 0 ? 0u : (uint32_t)SB;
-            cp_async_small<SB>(st + 2 * kKeys * CB + lane * SB, p.k_bscale + soff, sb);
-            cp_async_small<SB>(st + 2 * kKeys * CB + kKeys * SB + lane * SB, p.v_bscale + soff, sb);
+        for (int i = 0; i < CPR; ++i) {
+            const int s = __shfl_sync(0xffffffffu, id, i * RPI + lane / CPR);
+            const uint32_t bytes = s < 0 ? 0u : 16u;
+            const uint64_t off = (uint64_t)(uint32_t)max(s, 0) * row_codes;
+            rc::cp_async16(kdst + st + i * 512, kc + off, bytes, pol);
+            rc::cp_async16(vdst + st + v_row(i * RPI) * CB, vc + off, bytes, pol);
         }
+        const uint64_t soff = (uint64_t)(uint32_t)max(id, 0) * row_scales;
+        const uint32_t sb = ok ? (uint32_t)SB : 0u;
+        cp_async_small<SB>(sdst + st, ksc + soff, sb);
+        cp_async_small<SB>(sdst + st + kKeys * SB, vsc + soff, sb);
     };
-    int cur = slot_of(kStages), nxt;
+    {
+        int first[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-        issue(i, slot_of(i));
-        rc::cp_async_commit();
+        for (int i = 0; i < kStages; ++i) first[i] = slot_of(i);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) {
+            issue(i, first[i]);
+            rc::cp_async_commit();
+        }
     }
+    int cur = slot_of(kStages), nxt;
     // Q operand (f16): k-step ks of lane t covers dims t D/4 + 4 ks .. + 3
     uint32_t qb[KS][2];
     {
@@ -327,7 +429,114 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, 1) decode_fp4_kernel(const D
         sOwn[2 * t_lane + 1] = lse2(m_run[1], l_run[1]);
     }
     __syncwarp();
-    decode_epilogue<D, NC, FUSED, CROSS>(p, w, sE, sOwn, seg, first_row, lane);
+    if constexpr (FUSED) {
+        decode_epilogue<D, NC, FUSED, CROSS>(p, w, sE, sOwn, seg, first_row, lane);
+    } else {
+        // the partials belong to the preceding grid until it has ended
+        if (!waited) grid_dep_wait();
+        waited = true;
+        const int64_t idx = ((int64_t)(group + w.b) * p.kv_heads + w.kvh) * NC;
+        for (int c = 0; c < w.ncol; ++c)
+            for (int d = lane; d < D; d += 32) p.part_o[(idx + c) * D + d] = sE[c * D + d];
+        if (lane < w.ncol) p.part_lse[idx + lane] = sOwn[lane];
+        __syncwarp();  // the ring is refilled next
+    }
+    }
+    if (!FUSED && !waited) grid_dep_wait();
+}
+
+// Joins the partials of the split pass: a block per (row, head) (CROSS: per
+// (token, head), blockIdx.x = row * max_q + token and blockIdx.y the head), its
+// warps taking every kMergeWarps-th partial, the row's cascade segments first,
+// then the runs that touch it.
+template <int D, bool CROSS>
+__global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const DecParams p) {
+    constexpr int W = fp4::kMergeWarps, PER = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    int b, h, token = 0;
+    if constexpr (CROSS) {
+        b = blockIdx.x / p.max_q;
+        token = blockIdx.x % p.max_q;
+        h = blockIdx.y;
+    } else {
+        b = blockIdx.x / p.q_heads;
+        h = blockIdx.x % p.q_heads;
+    }
+    const RowKeys r = row_keys<CROSS>(p, b);
+    const int64_t orow = CROSS ? (int64_t)(r.qo0 + token) * p.q_heads + h : (int64_t)b * p.q_heads + h;
+    const int s0 = !CROSS && p.req_seg_indptr ? p.req_seg_indptr[b] : 0;
+    int n_seg = !CROSS && p.req_seg_indptr ? (p.req_seg_indptr[b + 1] - s0) * p.seg_chunks : 0;
+    grid_dep_wait();
+    if (CROSS && token * p.group >= r.ncol) return;
+    // a cascade kernel that gave up on a bounded wait left its partials unwritten
+    if (n_seg && p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout)) n_seg = 0;
+    const int g0 = r.L > 0 ? p.row_runs[2 * b] : 0, g1 = r.L > 0 ? p.row_runs[2 * b + 1] : -1;
+    const int n_all = n_seg + g1 - g0 + 1;
+    const int kvh = h / p.group, nc = CROSS ? 8 : p.group, col = token * p.group + h % p.group;
+    // lane l looks up the l-th of a round of 32 and its log-sum-exp, then all
+    // lanes read the rows (independent loads), against a running maximum
+    float m = -INFINITY, wsum = 0.f, acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+    for (int j0 = warp; j0 < n_all; j0 += 32 * W) {
+        const int j = j0 + lane * W;
+        const bool in_seg = j < n_seg;
+        int64_t row = 0;
+        if (in_seg)
+            row = ((int64_t)p.req_seg_pos[s0 + j / p.seg_chunks] * p.q_heads + h) * p.seg_chunks + j % p.seg_chunks;
+        else if (j < n_all)
+            row = ((int64_t)(g0 + b + j - n_seg) * p.kv_heads + kvh) * nc + col;
+        const float l2 = j < n_all ? (in_seg ? p.seg_lse : p.part_lse)[row] : -INFINITY;
+        const float* src = (in_seg ? p.seg_o : p.part_o) + row * D;
+        float mb = fmaxf(m, l2);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, k));
+        if (mb == -INFINITY) continue;
+        const float a = m == -INFINITY ? 0.f : rc::fast_exp2(m - mb);
+        wsum *= a;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] *= a;
+        m = mb;
+        const float wt = l2 == -INFINITY ? 0.f : rc::fast_exp2(l2 - m);
+        const int nb = min(32, (n_all - j0 + W - 1) / W);
+#pragma unroll 8
+        for (int i = 0; i < nb; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, wt, i);
+            const float* s = reinterpret_cast<const float*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+            wsum += wi;
+            if (wi != 0.f) {  // a partial without keys is not written
+#pragma unroll
+                for (int k = 0; k < PER; ++k) acc[k] += wi * s[lane + 32 * k];
+            }
+        }
+    }
+    __shared__ float sM[W], sW[W], sA[W][D];
+    if (lane == 0) {
+        sM[warp] = m;
+        sW[warp] = wsum;
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) sA[warp][lane + 32 * k] = acc[k];
+    __syncthreads();
+    float mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) mt = fmaxf(mt, sM[i]);
+    float total = 0.f, e[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        e[i] = sM[i] == -INFINITY ? 0.f : rc::fast_exp2(sM[i] - mt);
+        total += e[i] == 0.f ? 0.f : e[i] * sW[i];
+    }
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    for (int d = threadIdx.x; d < D; d += 32 * W) {
+        float o = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) o += e[i] == 0.f ? 0.f : e[i] * sA[i][d];
+        p.out[orow * D + d] = __float2bfloat16_rn(o * inv);
+    }
+    if (p.lse && threadIdx.x == 0) p.lse[orow] = total > 0.f ? (mt + log2f(total)) * rc::kLn2 : -INFINITY;
 }
 
 }  // namespace rc_dec
