@@ -422,10 +422,37 @@ def _tp(t):
     return C.c_void_p(t.data_ptr())
 
 
+def _ptr(t):
+    """_tp as a plain integer (None -> None): what the per-step calls pass."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"expected a contiguous tensor, got shape {tuple(t.shape)} strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _bytes(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
+
+
 def _stream(stream):
+    """Handle of a stream, the current device's current one by default (read
+    without building a Stream object: a step's calls are a few microseconds)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_device(call, *tensors):
+    """The kernels run on the current device and read these tensors there."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{call}: a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def make_pool_desc(k, v, err=None, mla: bool = False, head_dim_v: int | None = None, k_scale=None,
@@ -543,23 +570,21 @@ def make_rope_desc(cos_sin, interleaved: bool = False, offset: int = 0) -> rc_ro
     return r
 
 
-def _rows(name, t, n, heads, dim, write=False):
-    """(pointer, stride between tokens) of bf16 rows [n, heads, dim], each row
+def _rows(name, t, n, heads, dim, bf16, write=False):
+    """Stride between tokens of bf16 rows [n, heads, dim], each token's rows
     dense; tokens may be further apart (a slice of a projection's output)."""
-    if t is None:
-        return None, 0
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != dim or (heads and t.shape[1] != heads):
-        raise ValueError(f"{name}: expected [{n}, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
-    if t.element_size() != 2 or not t.is_floating_point():
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name}: expected [{n}, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.dtype is not bf16:
         raise ValueError(f"{name}: expected bf16, got {t.dtype}")
     s0, s1, s2 = t.stride()
     if n <= 1:
-        s0 = t.shape[1] * dim
-    if (dim > 1 and s2 != 1) or (t.shape[1] > 1 and s1 != dim):
+        s0 = heads * dim
+    if s2 != 1 or (s1 != dim and heads > 1):
         raise ValueError(f"{name}: each token's rows must be dense, got strides {t.stride()}")
-    if write and s0 < t.shape[1] * dim:
+    if write and s0 < heads * dim:
         raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
-    return C.c_void_p(t.data_ptr()), s0
+    return s0
 
 
 def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_new, v_new, q=None, q_out=None,
@@ -568,15 +593,30 @@ def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_ne
     header).  k_new, v_new [n, Hkv, d], q, q_out [n, Hq, d]: bf16, token strides
     of their own; v_new None for a latent pool; q_out None rotates q in place.
     slots, positions: int32 [n]."""
-    n, d = int(slots.numel()), pool.head_dim_k
-    if positions.numel() != n or slots.element_size() != 4 or positions.element_size() != 4:
+    import torch
+    bf16 = torch.bfloat16
+    n, hkv, d = slots.numel(), pool.kv_heads, pool.head_dim_k
+    if positions.numel() != n or slots.dtype is not torch.int32 or positions.dtype is not torch.int32:
         raise ValueError("kv_store_rope: slots and positions are int32 of one length")
-    kp, ks = _rows("k_new", k_new, n, pool.kv_heads, d)
-    vp, vs = _rows("v_new", v_new, n, pool.kv_heads, d)
-    qp, qs = _rows("q", q, n, 0, d, write=q_out is None)
-    op, os_ = (qp, qs) if q_out is None else _rows("q_out", q_out, n, q.shape[1], d, write=True)
-    st = lib().kv_store_rope(C.byref(pool), C.byref(rope), _tp(slots), _tp(positions), kp, ks, vp, vs, n, qp, qs,
-                             0 if q is None else int(q.shape[1]), op, os_, _tp(table), _tp(table_pos),
+    ks = _rows("k_new", k_new, n, hkv, d, bf16)
+    vs = _rows("v_new", v_new, n, hkv, d, bf16) if v_new is not None else 0
+    hq = qs = os_ = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q: expected [{n}, heads, {d}], got {tuple(q.shape)}")
+        hq = q.shape[1]
+        qs = _rows("q", q, n, hq, d, bf16, q_out is None)
+        if q_out is None:
+            q_out, os_ = q, qs
+        else:
+            os_ = _rows("q_out", q_out, n, hq, d, bf16, True)
+    elif q_out is not None:
+        raise ValueError("kv_store_rope: q_out without q")
+    _on_device("kv_store_rope", slots, positions, k_new, v_new, q, q_out, table, table_pos)
+    st = lib().kv_store_rope(C.byref(pool), C.byref(rope), _ptr(slots), _ptr(positions), k_new.data_ptr(), ks,
+                             v_new.data_ptr() if v_new is not None else None, vs, n,
+                             q.data_ptr() if hq else None, qs, hq, q_out.data_ptr() if hq else None, os_,
+                             _ptr(table), _ptr(table_pos),
                              _stream(stream))
     _check("kv_store_rope", st)
 
@@ -591,9 +631,9 @@ def attn_decode_workspace(desc: rc_attn_desc, batch: int, max_len: int, cascade:
 
 def attn_decode(desc: rc_attn_desc, q, kv: rc_kv_table, batch: int, out, lse=None, ws=None,
                 cascade: rc_cascade | None = None, stream=None):
-    st = lib().attn_decode(C.byref(desc), _tp(q), C.byref(kv), int(batch),
-                           C.byref(cascade) if cascade is not None else None, _tp(out), _tp(lse), _tp(ws),
-                           int(ws.numel() * ws.element_size()) if ws is not None else 0, _stream(stream))
+    st = lib().attn_decode(C.byref(desc), _ptr(q), C.byref(kv), int(batch),
+                           C.byref(cascade) if cascade is not None else None, _ptr(out), _ptr(lse), _ptr(ws),
+                           _bytes(ws), _stream(stream))
     _check("attn_decode", st)
 
 
@@ -646,9 +686,8 @@ def attn_extend_workspace(desc: rc_attn_desc, batch: int, max_q: int, max_len: i
 
 def attn_extend(desc: rc_attn_desc, q, qo_indptr, kv: rc_kv_table, batch: int, max_q: int, out, lse=None,
                 ws=None, stream=None):
-    st = lib().attn_extend(C.byref(desc), _tp(q), _tp(qo_indptr), C.byref(kv), int(batch), int(max_q), _tp(out),
-                           _tp(lse), _tp(ws), int(ws.numel() * ws.element_size()) if ws is not None else 0,
-                           _stream(stream))
+    st = lib().attn_extend(C.byref(desc), _ptr(q), _ptr(qo_indptr), C.byref(kv), int(batch), int(max_q), _ptr(out),
+                           _ptr(lse), _ptr(ws), _bytes(ws), _stream(stream))
     _check("attn_extend", st)
 
 
@@ -662,9 +701,9 @@ def attn_cross_workspace(desc: rc_attn_desc, batch: int, max_q: int, max_len: in
 def attn_cross(desc: rc_attn_desc, q, qo_indptr, kv: rc_kv_table, batch: int, max_q: int, out, lse=None,
                ws=None, stream=None):
     """Every token of row b over all the keys of the row (see the header)."""
-    st = lib().attn_cross(C.byref(desc), _tp(q), _tp(qo_indptr), C.byref(kv), int(batch), int(max_q), _tp(out),
-                          _tp(lse), _tp(ws), int(ws.numel() * ws.element_size()) if ws is not None else 0,
-                          _stream(stream))
+    _on_device("attn_cross", q, qo_indptr, out, lse, ws)
+    st = lib().attn_cross(C.byref(desc), _ptr(q), _ptr(qo_indptr), C.byref(kv), batch, max_q, _ptr(out), _ptr(lse),
+                          _ptr(ws), _bytes(ws), _stream(stream))
     _check("attn_cross", st)
 
 

@@ -272,6 +272,9 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
                  : run<64, rc::kFmtBf16>(pl, G, dp, mp, batch, max_q, st);
     if (e != cudaSuccess) return RC_ERR_CUDA;
     if (pl.n_chunks == 1 && !pl.runs) return RC_OK;
+    if (pl.runs)
+        return rc_host::launch_status(wide ? launch_merge_runs<128, true>(dp, max_rows, st)
+                                           : launch_merge_runs<64, true>(dp, max_rows, st));
     // the merge starts as the pass's CTAs leave and waits for its end inside
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)max_rows);
@@ -282,12 +285,6 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (pl.runs) {
-        cfg.gridDim = dim3((unsigned)max_rows, desc->q_heads);
-        cfg.blockDim = dim3(32 * fp4::kMergeWarps);
-        e = cudaLaunchKernelEx(&cfg, wide ? merge_runs_kernel<128, true> : merge_runs_kernel<64, true>, dp);
-        return rc_host::launch_status(e);
-    }
     e = cudaLaunchKernelEx(&cfg, wide ? cross_merge_kernel<128> : cross_merge_kernel<64>, (const float*)part_o,
                            (const float*)part_lse, pl.n_chunks, qo_indptr, max_q, max_rows, desc->q_heads,
                            static_cast<__nv_bfloat16*>(out), lse, (const int32_t*)P.err);

@@ -447,6 +447,9 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     if (!ok) return RC_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return RC_ERR_CUDA;
     if (pl.fused) return RC_OK;
+    if (fmt == rc::kFmtFp4)
+        return rc_host::launch_status(D == 128 ? launch_merge_runs<128, false>(dp, batch, st)
+                                               : launch_merge_runs<64, false>(dp, batch, st));
     const int32_t* ri = use_casc ? casc->req_seg_indptr : nullptr;
     const int32_t* rp = use_casc ? casc->req_seg_pos : nullptr;
     const unsigned nbh = (unsigned)batch * desc->q_heads;
@@ -455,16 +458,14 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     // inside), so its CTAs start as the split pass's leave
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(nbh);
-    cfg.blockDim = dim3(fmt == rc::kFmtFp4 ? 32 * fp4::kMergeWarps : 32);
+    cfg.blockDim = dim3(32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (fmt == rc::kFmtFp4)
-        e = cudaLaunchKernelEx(&cfg, D == 128 ? merge_runs_kernel<128, false> : merge_runs_kernel<64, false>, dp);
-    else if (D == 128)
+    if (D == 128)
         e = cudaLaunchKernelEx(&cfg, merge_kernel<128>, (const float*)dp.part_o, (const float*)dp.part_lse,
                                dp.n_chunks, dp.chunk, dp.len, (const float*)seg_o, (const float*)seg_lse,
                                pl.seg_chunks, ri, rp, desc->q_heads, dp.start, dp.table_len, o, lse, P.err);

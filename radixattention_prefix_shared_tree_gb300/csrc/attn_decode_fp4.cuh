@@ -23,6 +23,8 @@
 #include "attn_decode.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace rc_dec {
 
 namespace fp4 {
@@ -80,7 +82,7 @@ RC_DEV int v_row(int m) { return (m & 16) | ((m & 14) >> 1) | ((m & 1) << 3); }
 template <int D>
 RC_DEV int v_swz(int r) { return D == 128 ? (r & 2) : 0; }
 
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 
 }  // namespace fp4
 
@@ -165,13 +167,14 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
             }
         }
     }
+    const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
     const uint64_t pol = rc::l2_policy_evict_first();  // a request's own keys are read once per step
     const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.pool_k) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
     const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.pool_v) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
     const uint8_t* ksc = p.k_bscale + (int64_t)w.kvh * SB;
     const uint8_t* vsc = p.v_bscale + (int64_t)w.kvh * SB;
     const uint32_t row_codes = (uint32_t)p.kv_heads * CB, row_scales = (uint32_t)p.kv_heads * SB;
-    const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);
+    const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);  // at least 1 (checked by the host)
     // where this lane's copies of instruction 0 go; instruction i's are a
     // constant further: RPI rows of K, and the same rows' places in V
     const uint32_t kdst = rc::smem_u32(wbase) + lane * 16;
@@ -216,19 +219,19 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     auto issue = [&](int t, int slot) {
         if (t >= n_tiles) return;
         const uint32_t st = (t % kStages) * STAGE;
-        // an id outside the pool reads as a row of zeros (flagged)
+        // past the end, and for an id outside the pool (flagged), the scales
+        // are zeros, so the row reads as zeros whatever its codes: slot 0's
         const bool ok = (uint32_t)slot < n_slots;
         if (!ok && t * kKeys + lane < count) rc::flag_error(p.err, rc::kErrBadSlot);
-        const int id = ok ? slot : -1;
+        const int id = ok ? slot : 0;
 #pragma unroll
         for (int i = 0; i < CPR; ++i) {
             const int s = __shfl_sync(0xffffffffu, id, i * RPI + lane / CPR);
-            const uint32_t bytes = s < 0 ? 0u : 16u;
-            const uint64_t off = (uint64_t)(uint32_t)max(s, 0) * row_codes;
-            rc::cp_async16(kdst + st + i * 512, kc + off, bytes, pol);
-            rc::cp_async16(vdst + st + v_row(i * RPI) * CB, vc + off, bytes, pol);
+            const uint64_t off = (uint64_t)(uint32_t)s * row_codes;
+            rc::cp_async16(kdst + st + i * 512, kc + off, 16u, pol);
+            rc::cp_async16(vdst + st + v_row(i * RPI) * CB, vc + off, 16u, pol);
         }
-        const uint64_t soff = (uint64_t)(uint32_t)max(id, 0) * row_scales;
+        const uint64_t soff = (uint64_t)(uint32_t)id * row_scales;
         const uint32_t sb = ok ? (uint32_t)SB : 0u;
         cp_async_small<SB>(sdst + st, ksc + soff, sb);
         cp_async_small<SB>(sdst + st + kKeys * SB, vsc + soff, sb);
@@ -244,14 +247,19 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         }
     }
     int cur = slot_of(kStages), nxt;
-    // Q operand (f16): k-step ks of lane t covers dims t D/4 + 4 ks .. + 3
+    // Q operand (f16): k-step ks of lane t covers dims t D/4 + 4 ks .. + 3.  The
+    // scale's sign goes into Q, so that the largest score is the largest
+    // scaled one; a scale of 0 becomes one too small to matter, which keeps a
+    // masked score (-infinity) what it is.
     uint32_t qb[KS][2];
     {
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const bool hv = g_lane < w.ncol;
         const uint4* qrow = reinterpret_cast<const uint4*>(p.q + w.qrow<CROSS>(hv ? g_lane : 0) * D + t_lane * (D / 4));
 #pragma unroll
         for (int j = 0; j < KS / 2; ++j) {
-            const uint4 x = hv ? __ldg(qrow + j) : make_uint4(0, 0, 0, 0);
+            uint4 x = hv ? __ldg(qrow + j) : make_uint4(0, 0, 0, 0);
+            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
             qb[2 * j][0] = rc::bf16x2_to_f16x2(x.x);
             qb[2 * j][1] = rc::bf16x2_to_f16x2(x.y);
             qb[2 * j + 1][0] = rc::bf16x2_to_f16x2(x.z);
@@ -261,7 +269,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     float o[KS][4];
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float m_run[2] = {-INFINITY, -INFINITY};
+    float2 l_run = make_float2(0.f, 0.f);
 
     for (int t = 0; t < n_tiles; ++t) {
         rc::cp_async_wait<kStages - 1>();
@@ -293,20 +302,18 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
                 s0[0] = s0[1] = rc::scale_pair<0, 0>(sKs[r0 * SB + t_lane]);
                 s1[0] = s1[1] = rc::scale_pair<0, 0>(sKs[r1 * SB + t_lane]);
             }
-            float e[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+            s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < KS / 2; ++j) {  // a word: two k-steps
-                const int sc = j / (KS / 4);
+                const int bl = j / (KS / 4);
                 uint32_t a0, a2, c0, c2, a1, a3, c1, c3;
                 rc::e2m1x8_to_f16x8(x0[j], a0, a2, c0, c2);
                 rc::e2m1x8_to_f16x8(x1[j], a1, a3, c1, c3);
-                rc::mma_f16_16816(e, rc::mul_f16x2(a0, s0[sc]), rc::mul_f16x2(a1, s1[sc]), rc::mul_f16x2(a2, s0[sc]),
-                                  rc::mul_f16x2(a3, s1[sc]), qb[2 * j][0], qb[2 * j][1]);
-                rc::mma_f16_16816(f, rc::mul_f16x2(c0, s0[sc]), rc::mul_f16x2(c1, s1[sc]), rc::mul_f16x2(c2, s0[sc]),
-                                  rc::mul_f16x2(c3, s1[sc]), qb[2 * j + 1][0], qb[2 * j + 1][1]);
+                rc::mma_f16_16816(s[half], rc::mul_f16x2(a0, s0[bl]), rc::mul_f16x2(a1, s1[bl]), rc::mul_f16x2(a2, s0[bl]),
+                                  rc::mul_f16x2(a3, s1[bl]), qb[2 * j][0], qb[2 * j][1]);
+                rc::mma_f16_16816(s[half], rc::mul_f16x2(c0, s0[bl]), rc::mul_f16x2(c1, s1[bl]), rc::mul_f16x2(c2, s0[bl]),
+                                  rc::mul_f16x2(c3, s1[bl]), qb[2 * j + 1][0], qb[2 * j + 1][1]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[half][i] = (e[i] + f[i]) * p.scale_log2;
         }
         if (t == n_tiles - 1) {  // keys past the end (their codes are zeros)
 #pragma unroll
@@ -326,6 +333,7 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx *= sc;
             if (mx > m_run[j] + 8.f) {
                 alpha[j] = tc::ex2(m_run[j] - mx);  // 0 while nothing was seen
                 m_run[j] = mx;
@@ -333,8 +341,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
             }
         }
         if (__any_sync(0xffffffffu, grow)) {
-            l_run[0] *= alpha[0];
-            l_run[1] *= alpha[1];
+            l_run.x *= alpha[0];
+            l_run.y *= alpha[1];
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 o[i][0] *= alpha[0];
@@ -343,25 +351,24 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
                 o[i][3] *= alpha[1];
             }
         }
-        const float mu0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float mu1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        const float2 nmu = make_float2(m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]);
         uint32_t pb[2][2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const float p0 = tc::ex2(s[half][0] - mu0), p1 = tc::ex2(s[half][1] - mu1);
-            const float p2 = tc::ex2(s[half][2] - mu0), p3 = tc::ex2(s[half][3] - mu1);
-            l_run[0] += p0 + p2;
-            l_run[1] += p1 + p3;
-            // P to f16 (11 bits, at most 2^8): the denominator keeps the fp32 terms
-            pb[half][0] = rc::movmatrix_trans(rc::pack_f16(p0, p1));
-            pb[half][1] = rc::movmatrix_trans(rc::pack_f16(p2, p3));
-        }
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 x = tc::ffma2(make_float2(s[half][2 * k], s[half][2 * k + 1]), sc, nmu);
+                const float2 e = make_float2(tc::ex2(x.x), tc::ex2(x.y));
+                l_run = tc::fadd2(l_run, e);
+                // P to f16 (11 bits, at most 2^8): the denominator keeps the fp32 terms
+                pb[half][k] = rc::movmatrix_trans(rc::pack_f16(e.x, e.y));
+            }
         // O^T += V^T P^T: lane group g holds dims g D/8 .. of keys 2t, 2t+1,
         // 2t+8, 2t+9; product mt takes dims g D/8 + 2 mt (row g) and + 1
         // (row g + 8): the two nibbles of byte mt
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            uint32_t x[4][KS / 4], sc[2];
+            uint32_t x[4][KS / 4], vs[2];
             uint32_t sb[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -377,8 +384,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
                     sb[k] = sVs[m * SB + (g_lane >> 1)];
                 }
             }
-            sc[0] = (sb[0] | (sb[1] << 16)) << 7;
-            sc[1] = (sb[2] | (sb[3] << 16)) << 7;
+            vs[0] = (sb[0] | (sb[1] << 16)) << 7;
+            vs[1] = (sb[2] | (sb[3] << 16)) << 7;
 #pragma unroll
             for (int j = 0; j < KS / 4; ++j) {
                 uint32_t a[2][2][4];  // [key pair][dim parity][byte]
@@ -392,8 +399,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    rc::mma_f16_16816(o[4 * j + i], rc::mul_f16x2(a[0][0][i], sc[0]), rc::mul_f16x2(a[0][1][i], sc[0]),
-                                      rc::mul_f16x2(a[1][0][i], sc[1]), rc::mul_f16x2(a[1][1][i], sc[1]), pb[half][0],
+                    rc::mma_f16_16816(o[4 * j + i], rc::mul_f16x2(a[0][0][i], vs[0]), rc::mul_f16x2(a[0][1][i], vs[0]),
+                                      rc::mul_f16x2(a[1][0][i], vs[1]), rc::mul_f16x2(a[1][1][i], vs[1]), pb[half][0],
                                       pb[half][1]);
             }
         }
@@ -406,15 +413,14 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     __syncwarp();
 
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 4);
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 8);
-        l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], 16);
+    for (int k = 4; k < 32; k <<= 1) {
+        l_run.x += __shfl_xor_sync(0xffffffffu, l_run.x, k);
+        l_run.y += __shfl_xor_sync(0xffffffffu, l_run.y, k);
     }
     float* sE = reinterpret_cast<float*>(wbase);
     float* sOwn = sE + 8 * D;
-    const float inv0 = l_run[0] > 0.f ? 1.f / l_run[0] : 0.f;
-    const float inv1 = l_run[1] > 0.f ? 1.f / l_run[1] : 0.f;
+    const float inv0 = l_run.x > 0.f ? 1.f / l_run.x : 0.f;
+    const float inv1 = l_run.y > 0.f ? 1.f / l_run.y : 0.f;
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
         const int d0 = g_lane * (D / 8) + 2 * mt;
@@ -425,8 +431,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     // merge turns the row into NaN instead of skipping the partial
     auto lse2 = [](float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; };
     if (g_lane == 0) {
-        sOwn[2 * t_lane] = lse2(m_run[0], l_run[0]);
-        sOwn[2 * t_lane + 1] = lse2(m_run[1], l_run[1]);
+        sOwn[2 * t_lane] = lse2(m_run[0], l_run.x);
+        sOwn[2 * t_lane + 1] = lse2(m_run[1], l_run.y);
     }
     __syncwarp();
     if constexpr (FUSED) {
@@ -445,40 +451,36 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     if (!FUSED && !waited) grid_dep_wait();
 }
 
-// Joins the partials of the split pass: a block per (row, head) (CROSS: per
-// (token, head), blockIdx.x = row * max_q + token and blockIdx.y the head), its
-// warps taking every kMergeWarps-th partial, the row's cascade segments first,
-// then the runs that touch it.
-template <int D, bool CROSS>
+// Joins the partials of the split pass, W warps per (row, head) (CROSS: per
+// (token, head)), each taking every W-th partial: the row's cascade segments
+// first, then the runs that touch it.  Rows with few partials get one warp,
+// long rows in many runs eight.  blockIdx.x is the row (CROSS: row * max_q +
+// token); blockIdx.y a group of kMergeWarps / W heads.
+template <int D, bool CROSS, int W>
 __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const DecParams p) {
-    constexpr int W = fp4::kMergeWarps, PER = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int V = D / 32;  // a lane's neighbouring columns
+    constexpr int HEADS = fp4::kMergeWarps / W;
+    using Vec = typename std::conditional<V == 4, float4, float2>::type;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, slot = (threadIdx.x >> 5) / W;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    int b, h, token = 0;
-    if constexpr (CROSS) {
-        b = blockIdx.x / p.max_q;
-        token = blockIdx.x % p.max_q;
-        h = blockIdx.y;
-    } else {
-        b = blockIdx.x / p.q_heads;
-        h = blockIdx.x % p.q_heads;
-    }
+    const int b = CROSS ? blockIdx.x / p.max_q : blockIdx.x, token = CROSS ? blockIdx.x % p.max_q : 0;
+    const int h = blockIdx.y * HEADS + slot;
     const RowKeys r = row_keys<CROSS>(p, b);
-    const int64_t orow = CROSS ? (int64_t)(r.qo0 + token) * p.q_heads + h : (int64_t)b * p.q_heads + h;
     const int s0 = !CROSS && p.req_seg_indptr ? p.req_seg_indptr[b] : 0;
     int n_seg = !CROSS && p.req_seg_indptr ? (p.req_seg_indptr[b + 1] - s0) * p.seg_chunks : 0;
     grid_dep_wait();
-    if (CROSS && token * p.group >= r.ncol) return;
+    const bool live = h < p.q_heads && (!CROSS || token * p.group < r.ncol);
+    if (W == 1 && !live) return;
     // a cascade kernel that gave up on a bounded wait left its partials unwritten
     if (n_seg && p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout)) n_seg = 0;
     const int g0 = r.L > 0 ? p.row_runs[2 * b] : 0, g1 = r.L > 0 ? p.row_runs[2 * b + 1] : -1;
-    const int n_all = n_seg + g1 - g0 + 1;
+    const int n_all = live ? n_seg + g1 - g0 + 1 : 0;
     const int kvh = h / p.group, nc = CROSS ? 8 : p.group, col = token * p.group + h % p.group;
     // lane l looks up the l-th of a round of 32 and its log-sum-exp, then all
     // lanes read the rows (independent loads), against a running maximum
-    float m = -INFINITY, wsum = 0.f, acc[PER];
+    float m = -INFINITY, wsum = 0.f, acc[V];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
     for (int j0 = warp; j0 < n_all; j0 += 32 * W) {
         const int j = j0 + lane * W;
         const bool in_seg = j < n_seg;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
         const float a = m == -INFINITY ? 0.f : rc::fast_exp2(m - mb);
         wsum *= a;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] *= a;
+        for (int k = 0; k < V; ++k) acc[k] *= a;
         m = mb;
         const float wt = l2 == -INFINITY ? 0.f : rc::fast_exp2(l2 - m);
         const int nb = min(32, (n_all - j0 + W - 1) / W);
@@ -507,36 +509,74 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
             wsum += wi;
             if (wi != 0.f) {  // a partial without keys is not written
+                const Vec v = reinterpret_cast<const Vec*>(s)[lane];
+                const float* x = reinterpret_cast<const float*>(&v);
 #pragma unroll
-                for (int k = 0; k < PER; ++k) acc[k] += wi * s[lane + 32 * k];
+                for (int k = 0; k < V; ++k) acc[k] += wi * x[k];
             }
         }
     }
-    __shared__ float sM[W], sW[W], sA[W][D];
-    if (lane == 0) {
-        sM[warp] = m;
-        sW[warp] = wsum;
+    if constexpr (W > 1) {  // the warps' sums, joined in their order
+        __shared__ float sM[fp4::kMergeWarps], sW[fp4::kMergeWarps];
+        __shared__ __align__(16) float sA[fp4::kMergeWarps][D];
+        const int me = slot * W + warp;
+        if (lane == 0) {
+            sM[me] = m;
+            sW[me] = wsum;
+        }
+        Vec v;
+        float* x = reinterpret_cast<float*>(&v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] = acc[k];
+        reinterpret_cast<Vec*>(sA[me])[lane] = v;
+        __syncthreads();
+        if (warp != 0 || !live) return;
+        m = -INFINITY;
+        wsum = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = fmaxf(m, sM[me + i]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float e = sM[me + i] == -INFINITY ? 0.f : rc::fast_exp2(sM[me + i] - m);
+            if (e == 0.f) continue;
+            wsum += e * sW[me + i];
+            const Vec u = reinterpret_cast<const Vec*>(sA[me + i])[lane];
+            const float* y = reinterpret_cast<const float*>(&u);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] += e * y[k];
+        }
     }
-#pragma unroll
-    for (int k = 0; k < PER; ++k) sA[warp][lane + 32 * k] = acc[k];
-    __syncthreads();
-    float mt = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < W; ++i) mt = fmaxf(mt, sM[i]);
-    float total = 0.f, e[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        e[i] = sM[i] == -INFINITY ? 0.f : rc::fast_exp2(sM[i] - mt);
-        total += e[i] == 0.f ? 0.f : e[i] * sW[i];
-    }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    for (int d = threadIdx.x; d < D; d += 32 * W) {
-        float o = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) o += e[i] == 0.f ? 0.f : e[i] * sA[i][d];
-        p.out[orow * D + d] = __float2bfloat16_rn(o * inv);
-    }
-    if (p.lse && threadIdx.x == 0) p.lse[orow] = total > 0.f ? (mt + log2f(total)) * rc::kLn2 : -INFINITY;
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const int64_t orow = CROSS ? (int64_t)(r.qo0 + token) * p.q_heads + h : (int64_t)b * p.q_heads + h;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (V / 2);
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(rc::pack_bf16(acc[0] * inv, acc[1] * inv),
+                                                    rc::pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+        *out = rc::pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = wsum > 0.f ? (m + log2f(wsum)) * rc::kLn2 : -INFINITY;
+}
+
+// rows: batch rows, or (CROSS) their tokens; as the split pass's programmatic
+// dependent, so that its blocks start as that pass's leave.
+template <int D, bool CROSS>
+cudaError_t launch_merge_runs(const DecParams& p, int64_t rows, cudaStream_t st) {
+    const int64_t parts = (p.n_chunks + (int64_t)p.batch) / p.batch;  // of a row, on average
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(32 * fp4::kMergeWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int w = parts <= 8 ? 1 : 8;
+    const int heads = fp4::kMergeWarps / w;
+    cfg.gridDim = dim3((unsigned)rows, (p.q_heads + heads - 1) / heads);
+    return w == 1 ? cudaLaunchKernelEx(&cfg, merge_runs_kernel<D, CROSS, 1>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_runs_kernel<D, CROSS, 8>, p);
 }
 
 }  // namespace rc_dec

@@ -231,7 +231,7 @@ inline int pool_format(const rc_pool_desc& p) {
 inline rc_status check_fp4(const rc_pool_desc& p) {
     if (p.mla || p.head_dim_k != p.head_dim_v || (p.head_dim_k != 128 && p.head_dim_k != 64))
         return RC_ERR_UNSUPPORTED;
-    if (!p.k || !p.v || !p.k_bscale || !p.v_bscale) return RC_ERR_ARG;
+    if (!p.k || !p.v || !p.k_bscale || !p.v_bscale || p.n_slots <= 0) return RC_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) |
          reinterpret_cast<uintptr_t>(p.k_bscale) | reinterpret_cast<uintptr_t>(p.v_bscale)) & 15)
         return RC_ERR_ARG;

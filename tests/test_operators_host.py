@@ -117,7 +117,7 @@ def test_kv_store_rope_binding_checks_shapes():
     for kw in bad:
         with pytest.raises(ValueError):
             ra.kv_store_rope(pool, r, **{**good, **kw})
-    assert ra._rows("q", wide[:, :32], 4, 32, 128)[1] == 48 * 128      # a slice of one projection's output
+    assert ra._rows("q", wide[:, :32], 4, 32, 128, BF) == 48 * 128      # a slice of one projection's output
     with pytest.raises(ValueError):
         ra.make_rope_desc(torch.zeros(4, 128, dtype=BF))
     with pytest.raises(ValueError):
