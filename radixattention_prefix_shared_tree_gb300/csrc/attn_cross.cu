@@ -151,8 +151,11 @@ cudaError_t launch_few(const DecParams& p, int smem, int batch, cudaStream_t st)
 template <int D, int FMT, bool FUSED>
 cudaError_t few(const DecParams& p, int batch, cudaStream_t st) {
     if constexpr (FMT == rc::kFmtFp4)
-        return launch_few<decode_fp4_kernel<D, kFewColumns, FUSED, true>, fp4::kWarps, !FUSED>(
-            p, fp4::smem_bytes<D>(), batch, st);
+        return p.kv_heads % fp4::kWarps == 0
+                   ? launch_few<decode_fp4_kernel<D, kFewColumns, FUSED, true, true>, fp4::kWarps, !FUSED>(
+                         p, fp4::smem_bytes<D, true>(), batch, st)
+                   : launch_few<decode_fp4_kernel<D, kFewColumns, FUSED, true, false>, fp4::kWarps, !FUSED>(
+                         p, fp4::smem_bytes<D, false>(), batch, st);
     else
         return launch_few<decode_split_kernel<D, kFewColumns, FUSED, FMT == rc::kFmtFp8, true>, kWarpsPerCta>(
             p, dec_smem_bytes<D, FMT == rc::kFmtFp8>(), batch, st);

@@ -235,8 +235,11 @@ cudaError_t launch_table(const DecParams& p, int smem, int batch, int kv_heads, 
 template <int D, int G, bool FUSED, int FMT>
 cudaError_t launch_split(const DecParams& p, int batch, int kv_heads, cudaStream_t st, bool after_cascade) {
     if constexpr (FMT == rc::kFmtFp4)
-        return launch_table<decode_fp4_kernel<D, G, FUSED, false>, fp4::kWarps, !FUSED>(p, fp4::smem_bytes<D>(), batch,
-                                                                               kv_heads, st, after_cascade);
+        return kv_heads % fp4::kWarps == 0
+                   ? launch_table<decode_fp4_kernel<D, G, FUSED, false, true>, fp4::kWarps, !FUSED>(
+                         p, fp4::smem_bytes<D, true>(), batch, kv_heads, st, after_cascade)
+                   : launch_table<decode_fp4_kernel<D, G, FUSED, false, false>, fp4::kWarps, !FUSED>(
+                         p, fp4::smem_bytes<D, false>(), batch, kv_heads, st, after_cascade);
     else
         return launch_table<decode_split_kernel<D, G, FUSED, FMT == rc::kFmtFp8>, kWarpsPerCta>(
             p, dec_smem_bytes<D, FMT == rc::kFmtFp8>(), batch, kv_heads, st, after_cascade);

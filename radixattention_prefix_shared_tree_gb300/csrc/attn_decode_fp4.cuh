@@ -32,7 +32,7 @@ namespace fp4 {
 constexpr int kKeys = 32;          // keys per tile: a lane's slot id each
 constexpr int kWarps = 4;          // per CTA
 constexpr int kCtasPerSm = 4;      // 16 warps' rings and registers fill an SM
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 template <int D>
 __host__ __device__ constexpr int code_bytes() { return D / 2; }
@@ -40,10 +40,14 @@ template <int D>
 __host__ __device__ constexpr int scale_bytes() { return D / 16; }
 template <int D>
 __host__ __device__ constexpr int stage_bytes() { return 2 * kKeys * (code_bytes<D>() + scale_bytes<D>()); }
+// One head's part of a stage that the CTA's warps fill together: padded so that
+// neighbouring heads' copies land in different banks.
 template <int D>
-__host__ __device__ constexpr int warp_bytes() { return kStages * stage_bytes<D>(); }
-template <int D>
-__host__ __device__ constexpr int smem_bytes() { return kWarps * warp_bytes<D>(); }
+__host__ __device__ constexpr int head_bytes() { return stage_bytes<D>() + code_bytes<D>(); }
+template <int D, bool COOP>
+__host__ __device__ constexpr int warp_bytes() { return kStages * (COOP ? head_bytes<D>() : stage_bytes<D>()); }
+template <int D, bool COOP>
+__host__ __device__ constexpr int smem_bytes() { return kWarps * warp_bytes<D, COOP>(); }
 
 // How the split pass divides a batch: all rows' keys, 32 to a tile, laid end to
 // end and cut into equal runs of tiles, one run per group of kv_heads warps (a
@@ -88,7 +92,15 @@ constexpr int kMergeWarps = 8;
 
 // FUSED: one item per warp, result written (and the row's cascade partials
 // folded in) by its epilogue.  Otherwise the equal runs described above.
-template <int D, int NC, bool FUSED, bool CROSS>
+//
+// COOP (kv_heads a multiple of 4): a CTA's four warps are four neighbouring
+// heads of the same keys and fill their ring together, a key's four code rows
+// as one 256-byte read and its four scale blocks as one 32-byte read (D = 128).
+// Apart, every warp reads 64 and 8 bytes of them, and the number of requests,
+// not their bytes, bounds the loads: at 256 rows of 512-5119 keys the loads
+// alone took 152 us against 123 without the scales' eight-byte reads.  Other
+// head counts keep a ring per warp.
+template <int D, int NC, bool FUSED, bool CROSS, bool COOP>
 __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_kernel(const DecParams p, int n_items) {
     using namespace fp4;
     static_assert(D == 128 || D == 64, "head_dim");
@@ -96,8 +108,10 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     constexpr int CB = code_bytes<D>(), SB = scale_bytes<D>();
     constexpr int CPR = CB / 16;               // 16-byte chunks per row
     constexpr int RPI = 32 / CPR;              // rows one instruction copies
-    constexpr int STAGE = stage_bytes<D>();
-    static_assert(warp_bytes<D>() >= epilogue_bytes<D, NC>(), "epilogue scratch");
+    constexpr int HS = head_bytes<D>();
+    constexpr int STAGE = COOP ? kWarps * HS : stage_bytes<D>();  // bytes from a warp's stage to its next
+    constexpr int AHEAD = COOP ? kStages - 1 : kStages;           // tiles in flight at a tile's start
+    static_assert(warp_bytes<D, COOP>() >= epilogue_bytes<D, NC>(), "epilogue scratch");
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g_lane = lane >> 2, t_lane = lane & 3;
@@ -107,7 +121,9 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         grid_dep_wait();
         return;
     }
-    unsigned char* wbase = smem + warp * warp_bytes<D>();
+    // this warp's first stage, and (once all warps are done with theirs) its scratch
+    unsigned char* wbase = smem + warp * (COOP ? HS : warp_bytes<D, COOP>());
+    unsigned char* scratch = smem + warp * warp_bytes<D, COOP>();
     Item w;
     SegParts seg{0, 0};
     int64_t first_row = 0;
@@ -169,25 +185,32 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     }
     const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
     const uint64_t pol = rc::l2_policy_evict_first();  // a request's own keys are read once per step
-    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.pool_k) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
-    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.pool_v) + (int64_t)w.kvh * CB + (lane % CPR) * 16;
-    const uint8_t* ksc = p.k_bscale + (int64_t)w.kvh * SB;
-    const uint8_t* vsc = p.v_bscale + (int64_t)w.kvh * SB;
     const uint32_t row_codes = (uint32_t)p.kv_heads * CB, row_scales = (uint32_t)p.kv_heads * SB;
     const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);  // at least 1 (checked by the host)
-    // where this lane's copies of instruction 0 go; instruction i's are a
-    // constant further: RPI rows of K, and the same rows' places in V
-    const uint32_t kdst = rc::smem_u32(wbase) + lane * 16;
-    const int vr0 = v_row(lane / CPR);
-    const uint32_t vdst = rc::smem_u32(wbase) + kKeys * CB + vr0 * CB + ((lane % CPR) ^ v_swz<D>(vr0)) * 16;
-    const uint32_t sdst = rc::smem_u32(wbase) + 2 * kKeys * CB + lane * SB;
+    // Code copy i of this thread is chunk c of key i * RPI + r: of this warp's
+    // head, or (COOP) of the CTA's head c / CPR.  Its place moves by a constant
+    // with i: RPI rows of K, and the same rows' places in V.  Scale copies: key
+    // `sr`, head offset `sh`.
+    const int r = COOP ? threadIdx.x / (kWarps * CPR) : lane / CPR;
+    const int c = COOP ? threadIdx.x % (kWarps * CPR) : lane % CPR;
+    const int sr = COOP ? threadIdx.x / kWarps : lane, sh = COOP ? threadIdx.x % kWarps : 0;
+    const int kvh0 = COOP ? w.kvh - warp : w.kvh;
+    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.pool_k) + (int64_t)kvh0 * CB + c * 16;
+    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.pool_v) + (int64_t)kvh0 * CB + c * 16;
+    const uint8_t* ksc = p.k_bscale + (int64_t)(kvh0 + sh) * SB;
+    const uint8_t* vsc = p.v_bscale + (int64_t)(kvh0 + sh) * SB;
+    const uint32_t ring = rc::smem_u32(COOP ? smem : wbase);
+    const int vr0 = v_row(r);
+    const uint32_t kdst = ring + (c / CPR) * HS + r * CB + (c % CPR) * 16;
+    const uint32_t vdst = ring + (c / CPR) * HS + kKeys * CB + vr0 * CB + ((c % CPR) ^ v_swz<D>(vr0)) * 16;
+    const uint32_t sdst = ring + sh * HS + 2 * kKeys * CB + sr * SB;
 
     while (run < run_end && (FUSED || (w.b >= 0 && w.b < p.batch))) {
     if constexpr (FUSED) {
         run = run_end;
     } else {  // the part of row w.b that lies in the run
-        const RowKeys r = row_keys<CROSS>(p, w.b);
-        row_tiles = (r.L + kKeys - 1) / kKeys;
+        const RowKeys rk = row_keys<CROSS>(p, w.b);
+        row_tiles = (rk.L + kKeys - 1) / kKeys;
         const int64_t lo = run - row_tile;
         if (lo >= row_tiles) {  // the run goes on in the next row
             row_tile += row_tiles;
@@ -195,11 +218,11 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
             continue;
         }
         const int64_t n = min((int64_t)row_tiles - lo, run_end - run);
-        w.row0 = r.row0;
-        w.ncol = CROSS ? r.ncol : NC;
-        w.qrow0 = CROSS ? (int64_t)r.qo0 * p.q_heads + w.kvh * p.group : (int64_t)w.b * p.q_heads + w.kvh * NC;
+        w.row0 = rk.row0;
+        w.ncol = CROSS ? rk.ncol : NC;
+        w.qrow0 = CROSS ? (int64_t)rk.qo0 * p.q_heads + w.kvh * p.group : (int64_t)w.b * p.q_heads + w.kvh * NC;
         w.k0 = (int)lo * kKeys;
-        w.count = (int)min((int64_t)r.L - w.k0, n * kKeys);
+        w.count = (int)min((int64_t)rk.L - w.k0, n * kKeys);
         if (lane == 0 && w.kvh == 0) {  // for the merge: the runs that touch the row
             if (lo == 0) p.row_runs[2 * w.b] = group;
             if (lo + n == row_tiles) p.row_runs[2 * w.b + 1] = group;
@@ -226,27 +249,28 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         const int id = ok ? slot : 0;
 #pragma unroll
         for (int i = 0; i < CPR; ++i) {
-            const int s = __shfl_sync(0xffffffffu, id, i * RPI + lane / CPR);
+            const int s = __shfl_sync(0xffffffffu, id, i * RPI + r);
             const uint64_t off = (uint64_t)(uint32_t)s * row_codes;
-            rc::cp_async16(kdst + st + i * 512, kc + off, 16u, pol);
+            rc::cp_async16(kdst + st + i * RPI * CB, kc + off, 16u, pol);
             rc::cp_async16(vdst + st + v_row(i * RPI) * CB, vc + off, 16u, pol);
         }
-        const uint64_t soff = (uint64_t)(uint32_t)id * row_scales;
-        const uint32_t sb = ok ? (uint32_t)SB : 0u;
+        const int sid = COOP ? __shfl_sync(0xffffffffu, ok ? slot : -1, sr) : ok ? slot : -1;
+        const uint64_t soff = (uint64_t)(uint32_t)max(sid, 0) * row_scales;
+        const uint32_t sb = sid >= 0 ? (uint32_t)SB : 0u;
         cp_async_small<SB>(sdst + st, ksc + soff, sb);
         cp_async_small<SB>(sdst + st + kKeys * SB, vsc + soff, sb);
     };
     {
-        int first[kStages];
+        int first[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) first[i] = slot_of(i);
+        for (int i = 0; i < AHEAD; ++i) first[i] = slot_of(i);
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             issue(i, first[i]);
             rc::cp_async_commit();
         }
     }
-    int cur = slot_of(kStages), nxt;
+    int cur = slot_of(AHEAD), nxt;
     // Q operand (f16): k-step ks of lane t covers dims t D/4 + 4 ks .. + 3.  The
     // scale's sign goes into Q, so that the largest score is the largest
     // scaled one; a scale of 0 becomes one too small to matter, which keeps a
@@ -273,9 +297,15 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     float2 l_run = make_float2(0.f, 0.f);
 
     for (int t = 0; t < n_tiles; ++t) {
-        rc::cp_async_wait<kStages - 1>();
-        __syncwarp();
-        nxt = slot_of(t + kStages + 1);
+        rc::cp_async_wait<AHEAD - 1>();
+        nxt = slot_of(t + AHEAD + 1);
+        if constexpr (COOP) {  // tile t is everyone's, and everyone is done with tile t - 1: refill its stage
+            __syncthreads();
+            issue(t + AHEAD, cur);
+            rc::cp_async_commit();
+        } else {
+            __syncwarp();
+        }
         const unsigned char* sK = wbase + (t % kStages) * STAGE;
         const unsigned char* sV = sK + kKeys * CB;
         const unsigned char* sKs = sV + kKeys * CB;
@@ -404,20 +434,23 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
                                       pb[half][1]);
             }
         }
-        __syncwarp();  // every lane has read tile t: its stage takes tile t + kStages
-        issue(t + kStages, cur);
-        rc::cp_async_commit();
+        if constexpr (!COOP) {
+            __syncwarp();  // every lane has read tile t: its stage takes tile t + kStages
+            issue(t + AHEAD, cur);
+            rc::cp_async_commit();
+        }
         cur = nxt;
     }
     rc::cp_async_wait<0>();
-    __syncwarp();
+    if constexpr (COOP) __syncthreads();
+    else __syncwarp();
 
 #pragma unroll
     for (int k = 4; k < 32; k <<= 1) {
         l_run.x += __shfl_xor_sync(0xffffffffu, l_run.x, k);
         l_run.y += __shfl_xor_sync(0xffffffffu, l_run.y, k);
     }
-    float* sE = reinterpret_cast<float*>(wbase);
+    float* sE = reinterpret_cast<float*>(scratch);
     float* sOwn = sE + 8 * D;
     const float inv0 = l_run.x > 0.f ? 1.f / l_run.x : 0.f;
     const float inv1 = l_run.y > 0.f ? 1.f / l_run.y : 0.f;
@@ -445,7 +478,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         for (int c = 0; c < w.ncol; ++c)
             for (int d = lane; d < D; d += 32) p.part_o[(idx + c) * D + d] = sE[c * D + d];
         if (lane < w.ncol) p.part_lse[idx + lane] = sOwn[lane];
-        __syncwarp();  // the ring is refilled next
+        if constexpr (COOP) __syncthreads();  // the ring is refilled next
+        else __syncwarp();
     }
     }
     if (!FUSED && !waited) grid_dep_wait();
