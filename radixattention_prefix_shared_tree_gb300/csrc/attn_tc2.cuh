@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
     uint64_t* o_done = p_full + 4;           // [QT], count 1
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int kvh = blockIdx.y, z = blockIdx.z;
     int blk = blockIdx.x;
     // cascade: launched as the programmatic dependent of whatever precedes it
@@ -724,52 +724,78 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
         }
         rc::cp_async_wait<0>();  // nothing in flight when the warp leaves
         if (!ok) rc::flag_error(p.err, rc::kErrTimeout);
-    } else if (lane == 0) {
+    } else {
         // ================================================= MMA (warp 8+NP)
-        // descriptors built once per operand and stepped along K by 32-bit adds
+        // The whole warp runs the loop and one elected lane issues, so that the
+        // descriptors (built once per operand, stepped along K by 32-bit adds)
+        // stay in uniform registers, where the instruction wants them: from a
+        // lane of its own each product cost ~85 cycles to issue against the
+        // ~53 (N = 64) and 64 (N = 128) that it runs.  A barrier's state is asked
+        // for before the products ahead of its use are issued, which hides
+        // the answer's ~60 cycles behind them.
+        const bool lead = tc::elect_one();
+        const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+        const int nt = __shfl_sync(0xffffffffu, n_tiles, 0), nq = __shfl_sync(0xffffffffu, n_qt, 0);
         const tc::Desc qd = tc::desc_halves(rc::smem_u32(sQ), 128, SB);
-        auto issue_s = [&](int t) {
-            const tc::Desc kd = tc::desc_halves(rc::smem_u32(sKV + (t % NS) * 2 * KV_BYTES), 128, SB);
-            for (int q = 0; q < n_qt; ++q) {
-                const uint32_t qlo = qd.lo + q * (TM * D * 2 / 16);
+        const tc::Desc kd = tc::desc_halves(rc::smem_u32(sKV), 128, SB);
+        const tc::Desc vd = tc::desc_halves(rc::smem_u32(sKV + KV_BYTES), SB, 128);
+        constexpr uint32_t STEP = 2 * KV_BYTES / 16;  // from a stage to the next
+        auto issue_s = [&](int t, int st) {
+            const uint32_t klo = kd.lo + st * STEP, ds = tb + (t & 1) * TN;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16_h(tbase + q * 256 + (t & 1) * TN, qlo + k * 16, qd.hi, kd.lo + k * 16, kd.hi, idS,
-                                   k > 0 ? 1u : 0u);
-                tc::commit(&s_full[q * 2 + (t & 1)]);
+            for (int q = 0; q < QT; ++q) {
+                if (q < nq && lead) {
+                    const uint32_t qlo = qd.lo + q * (TM * D * 2 / 16);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16_h(ds + q * 256, qlo + k * 16, qd.hi, klo + k * 16, kd.hi, idS, k > 0 ? 1u : 0u);
+                    tc::commit(&s_full[q * 2 + (t & 1)]);
+                }
             }
         };
-        ok = tc::mbar_wait(q_full, 0, kWaitIter);
-        if (ok && n_tiles > 0) {
-            ok = tc::mbar_wait(&kv_full[0], 0, kWaitIter);
+        // waits for a phase that `asked` may have seen complete already
+        auto wait = [&](uint32_t asked, uint64_t* bar_, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, asked != 0 || tc::mbar_wait(bar_, parity, kWaitIter));
             tc::fence_after();
-            tc::fence_proxy_async();  // the rows arrived through the generic proxy; the tensor core reads them
-            if (ok) issue_s(0);
+        };
+        wait(0, q_full, 0);
+        if (ok && nt > 0) {
+            wait(0, &kv_full[0], 0);
+            if constexpr (!F16) tc::fence_proxy_async();  // the rows came by cp.async; the tensor core reads them
+            if (ok) issue_s(0, 0);
         }
-        for (int t = 0; t < n_tiles && ok; ++t) {
-            const int s = t % NS;
-            if (t + 1 < n_tiles) {  // next tile's S products first: they run during this softmax
-                ok = tc::mbar_wait(&kv_full[(t + 1) % NS], ((t + 1) / NS) & 1, kWaitIter);
-                tc::fence_after();
-                tc::fence_proxy_async();
+        int st = 0, ph = 0;                // tile t's stage, and how often it was used before (parity)
+        for (int t = 0; t < nt && ok; ++t) {
+            const int st1 = st + 1 == NS ? 0 : st + 1, ph1 = st + 1 == NS ? ph ^ 1 : ph;
+            if (t + 1 < nt) {  // next tile's S products first: they run during this softmax
+                wait(0, &kv_full[st1], ph1);
+                if constexpr (!F16) tc::fence_proxy_async();
                 if (!ok) break;
-                issue_s(t + 1);
             }
-            const tc::Desc vd = tc::desc_halves(rc::smem_u32(sKV + s * 2 * KV_BYTES + KV_BYTES), SB, 128);
-            for (int q = 0; q < n_qt && ok; ++q) {
-                ok = tc::mbar_wait(&p_full[q * 2 + (t & 1)], (t >> 1) & 1, kWaitIter);
-                tc::fence_after();
-                if (!ok) break;
-                const uint32_t pt = tbase + q * 256 + (t & 1) * TN;  // P(t) in TMEM, 8 columns per 16 keys
+            uint32_t asked = tc::mbar_test(&p_full[t & 1], (t >> 1) & 1);
+            if (t + 1 < nt) issue_s(t + 1, st1);
+            const uint32_t vlo = vd.lo + st * STEP, acc = t > 0 ? 1u : 0u;
 #pragma unroll
-                for (int j = 0; j < TN / 16; ++j)
-                    tc::mma_bf16_ts_h(tbase + q * 256 + 128, pt + j * 8, vd.lo + j * (2 * SB / 16), vd.hi, idPV,
-                                      (t > 0 || j > 0) ? 1u : 0u);
-                tc::commit(&o_done[q]);
+            for (int q = 0; q < QT; ++q) {
+                if (q >= nq || !ok) break;
+                wait(asked, &p_full[q * 2 + (t & 1)], (t >> 1) & 1);
+                if (!ok) break;
+                if (q + 1 < nq) asked = tc::mbar_test(&p_full[(q + 1) * 2 + (t & 1)], (t >> 1) & 1);
+                const uint32_t pt = tb + q * 256 + (t & 1) * TN;  // P(t) in TMEM, 8 columns per 16 keys
+                if (lead) {
+#pragma unroll
+                    for (int j = 0; j < TN / 16; ++j)
+                        tc::mma_bf16_ts_h(tb + q * 256 + 128, pt + j * 8, vlo + j * (2 * SB / 16), vd.hi, idPV,
+                                          j > 0 ? 1u : acc);
+                    tc::commit(&o_done[q]);
+                }
             }
-            tc::commit(&kv_empty[s]);  // stage s is free once everything issued so far is done
+            if (lead) tc::commit(&kv_empty[st]);  // the stage is free once everything issued so far is done
+            st = st1;
+            ph = ph1;
         }
-        if (!ok) rc::flag_error(p.err, rc::kErrTimeout);
+        if (!ok && lead) rc::flag_error(p.err, rc::kErrTimeout);
+        __syncwarp();
     }
     if constexpr (MODE == rc::MQMode::kCascade) {
         if (p.early) {  // every thread of the CTA has waited and triggered before it leaves

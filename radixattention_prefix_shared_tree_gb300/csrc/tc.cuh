@@ -174,6 +174,13 @@ RC_DEV bool mbar_test(uint64_t* mbar, uint32_t parity) {
     return done != 0;
 }
 
+// True in one lane of a converged warp.
+RC_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+
 // TMEM allocation by one full warp; the address lands in *smem_slot.
 RC_DEV void tmem_alloc(uint32_t* smem_slot, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
