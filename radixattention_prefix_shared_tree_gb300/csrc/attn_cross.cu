@@ -168,7 +168,7 @@ cudaError_t many_group(const rc::MQParams& p, int batch, int max_q, cudaStream_t
     if (e != cudaSuccess) return e;
     constexpr int TPC = rc_tc2::ROWS / G;
     dim3 grid((max_q + TPC - 1) / TPC, p.kv_heads, batch * p.seg_chunks);
-    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCross, FMT><<<grid, rc_tc2::THREADS, smem, st>>>(p);
+    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kCross, FMT><<<grid, rc_tc2::threads<FMT>(), smem, st>>>(p);
     return cudaGetLastError();
 }
 

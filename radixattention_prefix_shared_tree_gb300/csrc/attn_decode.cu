@@ -276,7 +276,7 @@ cudaError_t launch_cascade(const rc::MQParams& p0, const rc_cascade* c, int kv_h
     // waits for it before reading anything)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(rc_tc2::THREADS);
+    cfg.blockDim = dim3(rc_tc2::threads<FMT>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -70,13 +70,6 @@ inline bool whole_rows(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t
     return 2 * batch * kv_heads >= (int64_t)kWarps * kCtasPerSm * sms && max_len <= 512;
 }
 
-// 4- or 8-byte asynchronous copy (block scales); src_bytes = 0 writes zeros.
-template <int N>
-RC_DEV void cp_async_small(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(N)
-                 : "memory");
-}
-
 // Shared-memory row of V's key m (0..31): inside each 16 keys the even ones
 // come first, so that the four key pairs that lanes read together lie in
 // neighbouring rows.
@@ -257,8 +250,8 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         const int sid = COOP ? __shfl_sync(0xffffffffu, ok ? slot : -1, sr) : ok ? slot : -1;
         const uint64_t soff = (uint64_t)(uint32_t)max(sid, 0) * row_scales;
         const uint32_t sb = sid >= 0 ? (uint32_t)SB : 0u;
-        cp_async_small<SB>(sdst + st, ksc + soff, sb);
-        cp_async_small<SB>(sdst + st + kKeys * SB, vsc + soff, sb);
+        rc::cp_async_small<SB>(sdst + st, ksc + soff, sb);
+        rc::cp_async_small<SB>(sdst + st + kKeys * SB, vsc + soff, sb);
     };
     {
         int first[AHEAD];

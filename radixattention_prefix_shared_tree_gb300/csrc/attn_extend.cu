@@ -24,7 +24,7 @@ cudaError_t launch_extend(const rc::MQParams& p, int batch, int max_q, int kv_he
     if (e != cudaSuccess) return e;
     constexpr int TPC = rc_tc2::ROWS / G;
     dim3 grid((max_q + TPC - 1) / TPC, kv_heads, batch);
-    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT><<<grid, rc_tc2::THREADS, smem, st>>>(p);
+    rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT><<<grid, rc_tc2::threads<FMT>(), smem, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -59,10 +59,14 @@ constexpr int ROWS = QT * TM;  // query rows per CTA
 constexpr int TN = 64;         // keys per tile
 constexpr int NS_BF16 = 5;     // K/V stages
 constexpr int NS_FP8 = 4;
-constexpr int NS_FP4 = 5;
-constexpr int NP = 2;          // producer warps (a third one measured no faster)
-constexpr int MMA_WARP = 8 + NP;
-constexpr int THREADS = 32 * (MMA_WARP + 1);
+constexpr int NS_FP4 = 4;
+// Producer warps: two keep up with bf16 tiles, which they copy asynchronously; a
+// third one measured no faster.  Codes pass through their registers, and two
+// warps took longer over a tile than its products take.
+template <int FMT>
+__host__ __device__ constexpr int producers() { return FMT == rc::kFmtBf16 ? 2 : 3; }
+template <int FMT>
+__host__ __device__ constexpr int threads() { return 32 * (8 + producers<FMT>() + 1); }
 constexpr uint32_t kWaitIter = 1u << 24;
 template <int FMT>
 __host__ __device__ constexpr int stages() {
@@ -71,10 +75,18 @@ __host__ __device__ constexpr int stages() {
 template <int FMT>
 __host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FMT>() + 4 + 4 + 2; }
 
+// 4-bit pool: a tile as the pool holds it (K codes, V codes, K scales, V
+// scales), and how many of them each producer warp has on their way or at hand.
+template <int D>
+__host__ __device__ constexpr int raw_bytes() { return 2 * TN * (D / 2 + D / 16); }
+constexpr int RAW = 1;
 template <int D, int FMT = rc::kFmtBf16>
 __host__ __device__ constexpr int smem_bytes() {
     return QT * TM * D * 2 + stages<FMT>() * 2 * TN * D * 2 +
-           (FMT == rc::kFmtFp8 ? stages<FMT>() * 2 * TN * 4 : 0) + n_bars<FMT>() * 8 + 16;
+           (FMT == rc::kFmtFp8   ? stages<FMT>() * 2 * TN * 4
+            : FMT == rc::kFmtFp4 ? producers<FMT>() * RAW * raw_bytes<D>()
+                                 : 0) +
+           n_bars<FMT>() * 8 + 16;
 }
 
 // The cascade path reads FP8 pools too.
@@ -87,10 +99,11 @@ using tc::max3;
 using tc::mbar_arrive;
 
 template <int D, int G, rc::MQMode MODE, int FMT = rc::kFmtBf16>
-__global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams p) {
+__global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::MQParams p) {
     constexpr bool FP8 = FMT == rc::kFmtFp8, FP4 = FMT == rc::kFmtFp4;
     constexpr bool F16 = FP8 || FP4;             // operands in f16, widened from codes
     static_assert(!FP8 || D == 128, "FP8 pools: head_dim 128");
+    constexpr int NP = producers<FMT>(), MMA_WARP = 8 + NP, THREADS = threads<FMT>();
     constexpr int NS = stages<FMT>();
     constexpr int kBars = n_bars<FMT>();
     constexpr int CH = D / 8;
@@ -103,7 +116,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
     unsigned char* sQ = smem;                                  // [QT][128 rows][D]
     unsigned char* sKV = sQ + QT * TM * D * 2;                 // [NS][K, V]
     float* sScale = reinterpret_cast<float*>(sKV + NS * 2 * KV_BYTES);  // FP8: [NS][K scales, V scales]
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sKV + NS * 2 * KV_BYTES + (FP8 ? NS * 2 * TN * 4 : 0));
+    unsigned char* sRaw = sKV + NS * 2 * KV_BYTES;                       // FP4: [NP][RAW] tiles of codes and scales
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sKV + NS * 2 * KV_BYTES +
+                                                (FP8 ? NS * 2 * TN * 4 : FP4 ? NP * RAW * raw_bytes<D>() : 0));
     uint64_t* q_full = bar + 0;              // count 8 (softmax warps)
     uint64_t* kv_full = bar + 1;             // [NS], count 32 (the lanes of the tile's producer warp)
     uint64_t* kv_empty = bar + 1 + NS;       // [NS], count 1 (MMA commit)
@@ -575,8 +590,99 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
                 sl[h2] = (t < n_tiles && key < key_count) ? __ldg(keys + key) : -1;
             }
         };
+        if constexpr (FP4) {
+            // Codes and scales come by cp.async into this warp's own RAW tiles, two
+            // of its tiles ahead, and are widened from there into the operand
+            // stage: with loads into registers a warp waited out their latency
+            // every tile (256 x (1792 + 32-64) extend 593 us against 461 with
+            // the loads left out).  Every value is exact in f16.
+            constexpr int CB = D / 2, SB4 = D / 16;
+            constexpr int CPR = CB / 16;         // 16-byte chunks per row
+            constexpr int RPI = 32 / CPR;        // rows one instruction copies
+            const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);
+            unsigned char* raw = sRaw + (warp - 8) * RAW * raw_bytes<D>();
+            // chunk c of row r lies at chunk c ^ swz(r): eight rows' equal chunks
+            // then touch every bank once
+            auto swz4 = [](int r) { return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1; };
+            auto fetch = [&](int t, const int (&sl)[2]) {
+                if (t < n_tiles) {
+                    unsigned char* dst = raw + ((t / NP) % RAW) * raw_bytes<D>();
+                    const int c = lane % CPR;
+#pragma unroll
+                    for (int i = 0; i < TN / RPI; ++i) {
+                        const int r = i * RPI + lane / CPR;
+                        const int s = __shfl_sync(0xffffffffu, sl[i * RPI >> 5], r & 31);
+                        const bool live = (uint32_t)s < n_slots;
+                        const int64_t off = ((int64_t)(live ? s : 0) * p.kv_heads + kvh) * CB + c * 16;
+                        const uint32_t d = rc::smem_u32(dst) + r * CB + ((c ^ swz4(r)) * 16);
+                        rc::cp_async16(d, reinterpret_cast<const unsigned char*>(p.pool_k) + off, 16u, pol);
+                        rc::cp_async16(d + TN * CB, reinterpret_cast<const unsigned char*>(p.pool_v) + off, 16u, pol);
+                    }
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {  // zero scales: past the end, and for a slot outside the pool
+                        const int key = lane + 32 * h2;
+                        const bool live = (uint32_t)sl[h2] < n_slots;
+                        if (!live && t * TN + key < key_count) rc::flag_error(p.err, rc::kErrBadSlot);
+                        const int64_t off = ((int64_t)(live ? sl[h2] : 0) * p.kv_heads + kvh) * SB4;
+                        const uint32_t d = rc::smem_u32(dst) + 2 * TN * CB + key * SB4;
+                        rc::cp_async_small<SB4>(d, p.k_bscale + off, live ? (uint32_t)SB4 : 0u);
+                        rc::cp_async_small<SB4>(d + TN * SB4, p.v_bscale + off, live ? (uint32_t)SB4 : 0u);
+                    }
+                }
+                rc::cp_async_commit();
+            };
+            // 32 codes under two scales per lane: eight neighbouring lanes hold
+            // eight keys' equal chunks, so a 16-byte f16 store of theirs is 128
+            // contiguous bytes
+            constexpr int LPR = D / 32, KPI = 32 / LPR;
+            const int krow = lane & (KPI - 1), cq = lane / KPI;
+            auto widen = [&](unsigned char* dst, const unsigned char* codes, const unsigned char* scales) {
+#pragma unroll
+                for (int i = 0; i < TN / KPI; ++i) {
+                    const int key = i * KPI + krow;
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + key * CB + ((cq ^ swz4(key)) * 16));
+                    const uint32_t c = *reinterpret_cast<const uint16_t*>(scales + key * SB4 + 2 * cq);
+                    const uint32_t s0 = rc::scale_pair<0, 0>(c), s1 = rc::scale_pair<1, 1>(c);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 8 codes: f16 chunk 4 cq + k
+                        uint4 f;
+                        rc::e2m1x8_to_f16x8(x[k], f.x, f.y, f.z, f.w);
+                        const uint32_t sc = k < 2 ? s0 : s1;
+                        f.x = rc::mul_f16x2(f.x, sc);
+                        f.y = rc::mul_f16x2(f.y, sc);
+                        f.z = rc::mul_f16x2(f.z, sc);
+                        f.w = rc::mul_f16x2(f.w, sc);
+                        *reinterpret_cast<uint4*>(dst + tc::cm_offset(key, 4 * cq + k, CH)) = f;
+                    }
+                }
+            };
+            int sl[2] = {sl_first[0], sl_first[1]}, ahead[2];
+#pragma unroll
+            for (int i = 0; i < RAW; ++i) {
+                fetch(t0 + i * NP, sl);
+                load_ids(t0 + (i + 1) * NP, sl);
+            }
+            for (int t = t0; t < n_tiles && ok; t += NP) {
+                const int s = t % NS;
+                load_ids(t + (RAW + 1) * NP, ahead);
+                if (t >= NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], ((t / NS) + 1) & 1, kWaitIter));
+                if (!ok) break;
+                rc::cp_async_wait<RAW - 1>();
+                __syncwarp();
+                const unsigned char* src = raw + ((t / NP) % RAW) * raw_bytes<D>();
+                unsigned char* dst = sKV + s * 2 * KV_BYTES;
+                widen(dst, src, src + 2 * TN * CB);
+                widen(dst + KV_BYTES, src + TN * CB, src + 2 * TN * CB + TN * SB4);
+                tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
+                mbar_arrive(&kv_full[s]);
+                __syncwarp();  // every lane has read the raw tile
+                fetch(t + RAW * NP, sl);
+                sl[0] = ahead[0], sl[1] = ahead[1];
+            }
+        }
         int sl[2] = {sl_first[0], sl_first[1]}, sl_next[2];
-        for (int t = t0; t < n_tiles && ok; t += NP) {
+        for (int t = FP4 ? n_tiles : t0; t < n_tiles && ok; t += NP) {
             const int s = t % NS;
             load_ids(t + NP, sl_next);
             if (t >= NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], ((t / NS) + 1) & 1, kWaitIter));
@@ -637,60 +743,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc2_kernel(const rc::MQParams
                     const int64_t row = (int64_t)(live ? slot : 0) * p.kv_heads + kvh;
                     tsc[key] = live ? __ldg(p.k_scale + row) : 0.f;
                     tsc[TN + key] = live ? __ldg(p.v_scale + row) : 0.f;
-                }
-                tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
-                mbar_arrive(&kv_full[s]);
-            }
-            if constexpr (FP4) {
-                // 16 bytes (32 codes) and their two block scales per lane: four
-                // lanes hold a 64-byte row, eight keys an instruction (D = 64:
-                // two lanes a row, sixteen keys).  The tile's K and V loads are
-                // all in flight together; every value is exact in f16.
-                constexpr int LPR = D / 32;          // lanes per row
-                constexpr int KPI = 32 / LPR;        // keys per instruction
-                constexpr int IT = TN / KPI;
-                const int krow = lane & (KPI - 1), cq = lane / KPI;
-                uint4 w4[2][IT];
-                uint32_t sc4[2][IT];
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const int key = i * KPI + krow;
-                    int slot = __shfl_sync(0xffffffffu, sl[i * KPI >> 5], key & 31);
-                    bool live = t * TN + key < key_count;
-                    if (live && (slot < 0 || (int64_t)slot >= p.n_slots)) {
-                        rc::flag_error(p.err, rc::kErrBadSlot);
-                        live = false;
-                    }
-                    const int64_t row = (int64_t)(live ? slot : 0) * p.kv_heads + kvh;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const unsigned char* src = reinterpret_cast<const unsigned char*>(m ? p.pool_v : p.pool_k);
-                        const uint8_t* ssrc = m ? p.v_bscale : p.k_bscale;
-                        w4[m][i] = live ? __ldg(reinterpret_cast<const uint4*>(src + row * (D / 2)) + cq)
-                                        : make_uint4(0, 0, 0, 0);
-                        sc4[m][i] = live ? __ldg(reinterpret_cast<const uint16_t*>(ssrc + row * (D / 16)) + cq) : 0u;
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    unsigned char* dst = m ? sV : sK;
-#pragma unroll
-                    for (int i = 0; i < IT; ++i) {
-                        const int key = i * KPI + krow;
-                        const uint32_t s0 = rc::scale_pair<0, 0>(sc4[m][i]), s1 = rc::scale_pair<1, 1>(sc4[m][i]);
-                        const uint32_t x[4] = {w4[m][i].x, w4[m][i].y, w4[m][i].z, w4[m][i].w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {  // 8 codes: f16 chunk 4 cq + c
-                            uint4 f;
-                            rc::e2m1x8_to_f16x8(x[c], f.x, f.y, f.z, f.w);
-                            const uint32_t sc = c < 2 ? s0 : s1;
-                            f.x = rc::mul_f16x2(f.x, sc);
-                            f.y = rc::mul_f16x2(f.y, sc);
-                            f.z = rc::mul_f16x2(f.z, sc);
-                            f.w = rc::mul_f16x2(f.w, sc);
-                            *reinterpret_cast<uint4*>(dst + tc::cm_offset(key, 4 * cq + c, CH)) = f;
-                        }
-                    }
                 }
                 tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
                 mbar_arrive(&kv_full[s]);

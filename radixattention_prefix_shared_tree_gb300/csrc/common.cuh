@@ -93,6 +93,12 @@ RC_DEV void prefetch_l2(const void* src, uint32_t bytes) {
 RC_DEV void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
+// 4- or 8-byte asynchronous copy (block scales); src_bytes = 0 writes zeros.
+template <int N>
+RC_DEV void cp_async_small(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(N)
+                 : "memory");
+}
 RC_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 RC_DEV void cp_async_wait() {
