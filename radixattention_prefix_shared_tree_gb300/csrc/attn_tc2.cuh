@@ -75,11 +75,13 @@ __host__ __device__ constexpr int stages() {
 template <int FMT>
 __host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FMT>() + 4 + 4 + 2; }
 
-// 4-bit pool: a tile as the pool holds it (K codes, V codes, K scales, V
-// scales), and how many of them each producer warp has on their way or at hand.
+// 4-bit pool: every producer warp takes every NP-th group of eight keys of every
+// tile.  Its part of a tile as the pool holds it (K codes, V codes, K scales, V
+// scales of RAW_ROWS keys), and how many of those it has on their way or at hand.
+constexpr int RAW_ROWS = 8 * ((TN / 8 + 2) / 3);
 template <int D>
-__host__ __device__ constexpr int raw_bytes() { return 2 * TN * (D / 2 + D / 16); }
-constexpr int RAW = 1;
+__host__ __device__ constexpr int raw_bytes() { return 2 * RAW_ROWS * (D / 2 + D / 16); }
+constexpr int RAW = 2;
 template <int D, int FMT = rc::kFmtBf16>
 __host__ __device__ constexpr int smem_bytes() {
     return QT * TM * D * 2 + stages<FMT>() * 2 * TN * D * 2 +
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     uint64_t* bar = reinterpret_cast<uint64_t*>(sKV + NS * 2 * KV_BYTES +
                                                 (FP8 ? NS * 2 * TN * 4 : FP4 ? NP * RAW * raw_bytes<D>() : 0));
     uint64_t* q_full = bar + 0;              // count 8 (softmax warps)
-    uint64_t* kv_full = bar + 1;             // [NS], count 32 (the lanes of the tile's producer warp)
+    uint64_t* kv_full = bar + 1;             // [NS], count 32 (the lanes of the tile's producer warp; FP4: of all)
     uint64_t* kv_empty = bar + 1 + NS;       // [NS], count 1 (MMA commit)
     uint64_t* s_full = bar + 1 + 2 * NS;     // [QT][2], count 1
     uint64_t* p_full = s_full + 4;           // [QT][2] (one per S buffer), count 4 (the tile's softmax warps)
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     if (tid == 0) {
         tc::mbar_init(q_full, 8);
         for (int s = 0; s < NS; ++s) {
-            tc::mbar_init(&kv_full[s], 32);
+            tc::mbar_init(&kv_full[s], FP4 ? 32 * NP : 32);
             tc::mbar_init(&kv_empty[s], 1);
         }
         for (int i = 0; i < 4; ++i) {
@@ -591,42 +593,53 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             }
         };
         if constexpr (FP4) {
-            // Codes and scales come by cp.async into this warp's own RAW tiles, two
-            // of its tiles ahead, and are widened from there into the operand
-            // stage: with loads into registers a warp waited out their latency
-            // every tile (256 x (1792 + 32-64) extend 593 us against 461 with
-            // the loads left out).  Every value is exact in f16.
+            // All producer warps widen every tile together: a stage is held from
+            // the start of its widening until P.V has read it, and one warp's
+            // ~2200 cycles for a tile were a third of that (extend 256 x
+            // (1792 + 32-64) 479 us).  Codes and scales come by cp.async into the
+            // warp's own RAW parts, two tiles ahead, and are widened from there
+            // into the operand stage.  Every value is exact in f16.
+            static_assert(NP == 3 && TN == 64, "groups of eight keys per warp");
             constexpr int CB = D / 2, SB4 = D / 16;
             constexpr int CPR = CB / 16;         // 16-byte chunks per row
             constexpr int RPI = 32 / CPR;        // rows one instruction copies
+            const int wi = warp - 8;
             const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);
-            unsigned char* raw = sRaw + (warp - 8) * RAW * raw_bytes<D>();
+            unsigned char* raw = sRaw + wi * RAW * raw_bytes<D>();
+            // the tile's key of this warp's row r: groups wi, wi + NP, ...
+            auto key_of = [&](int r) { return ((r >> 3) * NP + wi) * 8 + (r & 7); };
             // chunk c of row r lies at chunk c ^ swz(r): eight rows' equal chunks
             // then touch every bank once
             auto swz4 = [](int r) { return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1; };
-            auto fetch = [&](int t, const int (&sl)[2]) {
+            // lane r: the slot id of row r's key (-1: none)
+            auto id_of = [&](int t) -> int {
+                const int key = t * TN + key_of(lane);
+                return lane < RAW_ROWS && key_of(lane) < TN && t < n_tiles && key < key_count ? __ldg(keys + key) : -1;
+            };
+            auto fetch = [&](int t, int id) {
                 if (t < n_tiles) {
-                    unsigned char* dst = raw + ((t / NP) % RAW) * raw_bytes<D>();
+                    const uint32_t dst = rc::smem_u32(raw) + (t % RAW) * raw_bytes<D>();
                     const int c = lane % CPR;
+                    const bool live = (uint32_t)id < n_slots;
+                    if (!live && id != -1) rc::flag_error(p.err, rc::kErrBadSlot);
+                    const int safe = live ? id : 0;
 #pragma unroll
-                    for (int i = 0; i < TN / RPI; ++i) {
+                    for (int i = 0; i < (RAW_ROWS + RPI - 1) / RPI; ++i) {
                         const int r = i * RPI + lane / CPR;
-                        const int s = __shfl_sync(0xffffffffu, sl[i * RPI >> 5], r & 31);
-                        const bool live = (uint32_t)s < n_slots;
-                        const int64_t off = ((int64_t)(live ? s : 0) * p.kv_heads + kvh) * CB + c * 16;
-                        const uint32_t d = rc::smem_u32(dst) + r * CB + ((c ^ swz4(r)) * 16);
-                        rc::cp_async16(d, reinterpret_cast<const unsigned char*>(p.pool_k) + off, 16u, pol);
-                        rc::cp_async16(d + TN * CB, reinterpret_cast<const unsigned char*>(p.pool_v) + off, 16u, pol);
+                        const int s = __shfl_sync(0xffffffffu, safe, r & 31);
+                        const int64_t off = ((int64_t)s * p.kv_heads + kvh) * CB + c * 16;
+                        const uint32_t d = dst + r * CB + ((c ^ swz4(r)) * 16);
+                        if (RAW_ROWS % RPI == 0 || r < RAW_ROWS) {
+                            rc::cp_async16(d, reinterpret_cast<const unsigned char*>(p.pool_k) + off, 16u, pol);
+                            rc::cp_async16(d + RAW_ROWS * CB, reinterpret_cast<const unsigned char*>(p.pool_v) + off, 16u,
+                                           pol);
+                        }
                     }
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {  // zero scales: past the end, and for a slot outside the pool
-                        const int key = lane + 32 * h2;
-                        const bool live = (uint32_t)sl[h2] < n_slots;
-                        if (!live && t * TN + key < key_count) rc::flag_error(p.err, rc::kErrBadSlot);
-                        const int64_t off = ((int64_t)(live ? sl[h2] : 0) * p.kv_heads + kvh) * SB4;
-                        const uint32_t d = rc::smem_u32(dst) + 2 * TN * CB + key * SB4;
+                    if (lane < RAW_ROWS) {  // zero scales: past the end, and for a slot outside the pool
+                        const int64_t off = ((int64_t)safe * p.kv_heads + kvh) * SB4;
+                        const uint32_t d = dst + 2 * RAW_ROWS * CB + lane * SB4;
                         rc::cp_async_small<SB4>(d, p.k_bscale + off, live ? (uint32_t)SB4 : 0u);
-                        rc::cp_async_small<SB4>(d + TN * SB4, p.v_bscale + off, live ? (uint32_t)SB4 : 0u);
+                        rc::cp_async_small<SB4>(d + RAW_ROWS * SB4, p.v_bscale + off, live ? (uint32_t)SB4 : 0u);
                     }
                 }
                 rc::cp_async_commit();
@@ -634,14 +647,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             // 32 codes under two scales per lane: eight neighbouring lanes hold
             // eight keys' equal chunks, so a 16-byte f16 store of theirs is 128
             // contiguous bytes
-            constexpr int LPR = D / 32, KPI = 32 / LPR;
+            constexpr int KPI = 32 / (D / 32);
             const int krow = lane & (KPI - 1), cq = lane / KPI;
             auto widen = [&](unsigned char* dst, const unsigned char* codes, const unsigned char* scales) {
 #pragma unroll
-                for (int i = 0; i < TN / KPI; ++i) {
-                    const int key = i * KPI + krow;
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + key * CB + ((cq ^ swz4(key)) * 16));
-                    const uint32_t c = *reinterpret_cast<const uint16_t*>(scales + key * SB4 + 2 * cq);
+                for (int i = 0; i < (RAW_ROWS + KPI - 1) / KPI; ++i) {
+                    const int r = i * KPI + krow, key = key_of(r);
+                    if (r >= RAW_ROWS || key >= TN) continue;
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + r * CB + ((cq ^ swz4(r)) * 16));
+                    const uint32_t c = *reinterpret_cast<const uint16_t*>(scales + r * SB4 + 2 * cq);
                     const uint32_t s0 = rc::scale_pair<0, 0>(c), s1 = rc::scale_pair<1, 1>(c);
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -657,28 +671,29 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     }
                 }
             };
-            int sl[2] = {sl_first[0], sl_first[1]}, ahead[2];
+            int id = id_of(0), ahead;
 #pragma unroll
             for (int i = 0; i < RAW; ++i) {
-                fetch(t0 + i * NP, sl);
-                load_ids(t0 + (i + 1) * NP, sl);
+                fetch(i, id);
+                id = id_of(i + 1);
             }
-            for (int t = t0; t < n_tiles && ok; t += NP) {
-                const int s = t % NS;
-                load_ids(t + (RAW + 1) * NP, ahead);
-                if (t >= NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], ((t / NS) + 1) & 1, kWaitIter));
+            int s = 0, ph = 1;  // stage, and the parity of the wait for it (its first use waits for nothing)
+            for (int t = 0; t < n_tiles && ok; ++t) {
+                ahead = id_of(t + RAW + 1);
+                if (t >= NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], ph, kWaitIter));
                 if (!ok) break;
                 rc::cp_async_wait<RAW - 1>();
                 __syncwarp();
-                const unsigned char* src = raw + ((t / NP) % RAW) * raw_bytes<D>();
+                const unsigned char* src = raw + (t % RAW) * raw_bytes<D>();
                 unsigned char* dst = sKV + s * 2 * KV_BYTES;
-                widen(dst, src, src + 2 * TN * CB);
-                widen(dst + KV_BYTES, src + TN * CB, src + 2 * TN * CB + TN * SB4);
+                widen(dst, src, src + 2 * RAW_ROWS * CB);
+                widen(dst + KV_BYTES, src + RAW_ROWS * CB, src + 2 * RAW_ROWS * CB + RAW_ROWS * SB4);
                 tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
                 mbar_arrive(&kv_full[s]);
                 __syncwarp();  // every lane has read the raw tile
-                fetch(t + RAW * NP, sl);
-                sl[0] = ahead[0], sl[1] = ahead[1];
+                fetch(t + RAW, id);
+                id = ahead;
+                if (++s == NS) s = 0, ph ^= 1;
             }
         }
         int sl[2] = {sl_first[0], sl_first[1]}, sl_next[2];
