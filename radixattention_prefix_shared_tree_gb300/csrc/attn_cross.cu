@@ -248,6 +248,7 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     dp.table_len = mp.table_len = kv->table_len;
     dp.out = mp.out = static_cast<__nv_bfloat16*>(out);
     dp.lse = mp.lse = lse;
+    mp.out_wide = 1;
     dp.part_o = mp.part_o = part_o;
     dp.part_lse = mp.part_lse = part_lse;
     dp.chunk = mp.seg_chunk = pl.chunk;

@@ -85,6 +85,7 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
     p.table_len = kv->table_len;
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
+    p.out_wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     p.k_scale = fp8 ? P.k_scale : nullptr;
     p.v_scale = fp8 ? P.v_scale : nullptr;
     p.k_bscale = fmt == rc::kFmtFp4 ? P.k_bscale : nullptr;

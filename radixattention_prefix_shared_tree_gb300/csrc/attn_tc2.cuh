@@ -51,6 +51,8 @@
 #include "mq_attn.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace rc_tc2 {
 
 constexpr int QT = 2;          // query tiles per CTA
@@ -99,6 +101,96 @@ using tc::fadd2;
 using tc::ffma2;
 using tc::max3;
 using tc::mbar_arrive;
+
+// The 4-bit pool's producer warps.  All of them widen every tile together: a
+// stage is held from the start of its widening until P.V has read it, and one
+// warp's ~2200 cycles for a tile were a third of that.  Codes and scales come by
+// cp.async into the warp's own RAW parts, two tiles ahead, and are widened
+// from there into the operand stage.  Every value is exact in f16.
+template <int D, int NP>
+struct Fp4Feed {
+    static_assert(NP == 3 && TN == 64, "groups of eight keys per warp");
+    static constexpr int CB = D / 2, SB = D / 16, CH = D / 8;
+    static constexpr int CPR = CB / 16;        // 16-byte chunks per row
+    static constexpr int RPI = 32 / CPR;       // rows one instruction copies
+    const rc::MQParams& p;
+    const int32_t* keys;
+    int key_count, n_tiles, kvh, wi, lane;
+    unsigned char* raw;
+    uint32_t n_slots;
+    uint64_t pol;
+
+    // the tile's key of this warp's row r: groups wi, wi + NP, ...
+    RC_DEV int key_of(int r) const { return ((r >> 3) * NP + wi) * 8 + (r & 7); }
+    // chunk c of row r lies at chunk c ^ swz(r): eight rows' equal chunks then
+    // touch every bank once
+    RC_DEV static int swz(int r) { return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1; }
+    // lane r: the slot id of row r's key (-1: none)
+    RC_DEV int id_of(int t) const {
+        const int key = t * TN + key_of(lane);
+        return lane < RAW_ROWS && key_of(lane) < TN && t < n_tiles && key < key_count ? __ldg(keys + key) : -1;
+    }
+    RC_DEV void fetch(int t, int id) const {
+        if (t < n_tiles) {
+            const uint32_t dst = rc::smem_u32(raw) + (t % RAW) * raw_bytes<D>();
+            const int c = lane % CPR;
+            const bool live = (uint32_t)id < n_slots;
+            if (!live && id != -1) rc::flag_error(p.err, rc::kErrBadSlot);
+            const int safe = live ? id : 0;
+#pragma unroll
+            for (int i = 0; i < (RAW_ROWS + RPI - 1) / RPI; ++i) {
+                const int r = i * RPI + lane / CPR;
+                const int s = __shfl_sync(0xffffffffu, safe, r & 31);
+                const int64_t off = ((int64_t)s * p.kv_heads + kvh) * CB + c * 16;
+                const uint32_t d = dst + r * CB + ((c ^ swz(r)) * 16);
+                if (RAW_ROWS % RPI == 0 || r < RAW_ROWS) {
+                    rc::cp_async16(d, reinterpret_cast<const unsigned char*>(p.pool_k) + off, 16u, pol);
+                    rc::cp_async16(d + RAW_ROWS * CB, reinterpret_cast<const unsigned char*>(p.pool_v) + off, 16u, pol);
+                }
+            }
+            if (lane < RAW_ROWS) {  // zero scales: past the end, and for a slot outside the pool
+                const int64_t off = ((int64_t)safe * p.kv_heads + kvh) * SB;
+                const uint32_t d = dst + 2 * RAW_ROWS * CB + lane * SB;
+                rc::cp_async_small<SB>(d, p.k_bscale + off, live ? (uint32_t)SB : 0u);
+                rc::cp_async_small<SB>(d + RAW_ROWS * SB, p.v_bscale + off, live ? (uint32_t)SB : 0u);
+            }
+        }
+        rc::cp_async_commit();
+    }
+    // 32 codes under two scales per lane: eight neighbouring lanes hold eight
+    // keys' equal chunks, so a 16-byte f16 store of theirs is 128 contiguous
+    // bytes
+    RC_DEV void widen(unsigned char* dst, const unsigned char* codes, const unsigned char* scales) const {
+        constexpr int KPI = 32 / (D / 32);
+        const int krow = lane & (KPI - 1), cq = lane / KPI;
+#pragma unroll
+        for (int i = 0; i < (RAW_ROWS + KPI - 1) / KPI; ++i) {
+            const int r = i * KPI + krow, key = key_of(r);
+            if (r >= RAW_ROWS || key >= TN) continue;
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + r * CB + ((cq ^ swz(r)) * 16));
+            const uint32_t c = *reinterpret_cast<const uint16_t*>(scales + r * SB + 2 * cq);
+            const uint32_t s0 = rc::scale_pair<0, 0>(c), s1 = rc::scale_pair<1, 1>(c);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 8 codes: f16 chunk 4 cq + k
+                uint4 f;
+                rc::e2m1x8_to_f16x8(x[k], f.x, f.y, f.z, f.w);
+                const uint32_t sc = k < 2 ? s0 : s1;
+                f.x = rc::mul_f16x2(f.x, sc);
+                f.y = rc::mul_f16x2(f.y, sc);
+                f.z = rc::mul_f16x2(f.z, sc);
+                f.w = rc::mul_f16x2(f.w, sc);
+                *reinterpret_cast<uint4*>(dst + tc::cm_offset(key, 4 * cq + k, CH)) = f;
+            }
+        }
+    }
+    // tile t from its raw part into the operand stage at dst
+    RC_DEV void put(int t, unsigned char* dst) const {
+        const unsigned char* src = raw + (t % RAW) * raw_bytes<D>();
+        widen(dst, src, src + 2 * RAW_ROWS * CB);
+        widen(dst + TN * D * 2, src + RAW_ROWS * CB, src + 2 * RAW_ROWS * CB + RAW_ROWS * SB);
+    }
+};
 
 template <int D, int G, rc::MQMode MODE, int FMT = rc::kFmtBf16>
 __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::MQParams p) {
@@ -309,13 +401,59 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     // query tiles with at least one valid row
     const int n_qt = min(QT, ((min(n_rows_tok - tok0, TPC) * G) + TM - 1) / TM);
 
-    // producers: slot ids of their first tile, loaded before the set-up too
-    int sl_first[2] = {-1, -1};
-    if (warp >= 8 && warp < MMA_WARP) {
+    // Producers: their first tiles' copies go out before the set-up, which
+    // their latency then overlaps (a stage's first use waits for nothing).
+    // Keys here are shared: by the CTAs of the other row blocks, and (a cached
+    // prefix) by later steps -- keep them in L2.
+    const uint64_t pol = rc::l2_policy_evict_last();
+    const int t0 = warp - 8;  // this producer's first tile
+    auto load_ids = [&](int t, int (&sl)[2]) {
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
-            const int key = (warp - 8) * TN + lane + 32 * h2;
-            if (warp - 8 < n_tiles && key < key_count) sl_first[h2] = __ldg(keys + key);
+            const int key = t * TN + lane + 32 * h2;
+            sl[h2] = (t < n_tiles && key < key_count) ? __ldg(keys + key) : -1;
+        }
+    };
+    auto copy_tile = [&](int t, const int (&sl)[2]) {  // bf16 pool: tile t into its stage
+        // lane -> (key within an 8-key group, 16-byte column within a group of 4)
+        const int klo = lane & 7, csub = lane >> 3;
+        unsigned char* sK = sKV + (t % NS) * 2 * KV_BYTES;
+        unsigned char* sV = sK + KV_BYTES;
+#pragma unroll
+        for (int kg = 0; kg < TN / 8; ++kg) {
+            const int key = kg * 8 + klo;
+            int slot = __shfl_sync(0xffffffffu, sl[kg >> 2], (kg & 3) * 8 + klo);
+            uint32_t bytes = 16;
+            if (t * TN + key >= key_count) { slot = 0; bytes = 0; }
+            else if (slot < 0 || (int64_t)slot >= p.n_slots) {
+                rc::flag_error(p.err, rc::kErrBadSlot);
+                slot = 0;
+                bytes = 0;
+            }
+            // chunks c = 4 cg + csub: 512 bytes apart in the stage, 64 in the row
+            const int64_t base = ((int64_t)slot * p.kv_heads + kvh) * D + csub * 8;
+            const uint32_t off = tc::cm_offset(key, csub, CH);
+            rc::cp_async16_run<512, 64>(rc::smem_u32(sK) + off, p.pool_k + base, bytes, pol,
+                                        std::make_integer_sequence<int, CH / 4>{});
+            rc::cp_async16_run<512, 64>(rc::smem_u32(sV) + off, p.pool_v + base, bytes, pol,
+                                        std::make_integer_sequence<int, CH / 4>{});
+        }
+    };
+    const Fp4Feed<D, 3> feed{p, keys, key_count, n_tiles, kvh, t0, lane, sRaw + (FP4 ? t0 * RAW * raw_bytes<D>() : 0),
+                             (uint32_t)min(p.n_slots, (int64_t)0x7fffffff), pol};
+    int feed_id = -1, sl[2] = {-1, -1};
+    if (warp >= 8 && warp < MMA_WARP) {
+        if constexpr (FP4) {
+            int first[RAW];
+#pragma unroll
+            for (int i = 0; i < RAW; ++i) first[i] = feed.id_of(i);
+            feed_id = feed.id_of(RAW);
+#pragma unroll
+            for (int i = 0; i < RAW; ++i) feed.fetch(i, first[i]);
+        } else {
+            load_ids(t0, sl);
+            if constexpr (!F16)
+                if (t0 < n_tiles) copy_tile(t0, sl);
         }
     }
     if (warp < 8) {
@@ -519,50 +657,68 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                 }
             }
         }
-        // ---- epilogue: normalised O rows and their log-sum-exp.  Rows go out
-        // through shared memory so that each store instruction writes whole
-        // row segments: per 32 columns, the warp's 32x32 fp32 block is staged
-        // (16-byte chunks XOR-swizzled by row: conflict-free both ways) in
-        // this warp's 4 KB of the Q region -- free once the tile's last P.V
-        // is done, since every S product was issued before it -- and read
-        // back 8 lanes per row, 4 rows per instruction.
+        // ---- epilogue: normalised O rows and their log-sum-exp.  Each thread
+        // has a row; it goes out through the warp's 8 KB of its own query
+        // tile's Q (free once the tile's last P.V is done, since every S
+        // product was issued before it), so that a store instruction writes
+        // whole rows: a row's 16-byte chunks XOR-swizzled by the row, so that
+        // neither side meets a bank twice.  (Straight from the registers every
+        // instruction would touch 32 rows, one tag each: 2.6 us a CTA.)
         if (q < n_qt) {
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             const float lse2 = l_run > 0.f ? m_used + log2f(l_run) : -INFINITY;
-            float* stg = reinterpret_cast<float*>(sQ + warp * 4096);
-            const int k8 = lane & 7;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t vb[32];
-                tc::tmem_ld32_issue(tq + 128 + c * 32, vb);
-                tc::tmem_ld_wait(vb);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<float4*>(stg + lane * 32 + ((k ^ (lane & 7)) * 4)) =
-                        make_float4(__uint_as_float(vb[4 * k]) * inv, __uint_as_float(vb[4 * k + 1]) * inv,
-                                    __uint_as_float(vb[4 * k + 2]) * inv, __uint_as_float(vb[4 * k + 3]) * inv);
+            const bool whole = MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1);
+            unsigned char* stg = sQ + warp * 32 * D * 2;
+            // n 16-byte chunks of every row of the warp, staged, to row `rw` of dst
+            // (its rows `stride` 16-byte units apart)
+            auto write_rows = [&](auto n_, uint4* dst, int64_t stride, int64_t extra) {
+                constexpr int N = decltype(n_)::value;
                 __syncwarp();
 #pragma unroll
-                for (int pass = 0; pass < 8; ++pass) {
-                    const int rr = pass * 4 + (lane >> 3);
-                    const float4 f = *reinterpret_cast<const float4*>(stg + rr * 32 + ((k8 ^ (rr & 7)) * 4));
-                    const int rc_ = q * TM + (warp & 3) * 32 + rr;  // row within the CTA
-                    const int tk = tok0 + rc_ / G;
-                    const int hh = kvh * G + (rc_ % G);
+                for (int i = 0; i < N; ++i) {
+                    const int lr = i * (32 / N) + lane / N, c = lane % N;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stg + lr * N * 16 + ((c ^ (lr & 7)) * 16));
+                    const int cr = q * TM + (warp & 3) * 32 + lr, tk = tok0 + cr / G;  // row within the CTA, its token
                     if (!ok || tk >= n_rows_tok) continue;
-                    if (MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1)) {
-                        uint2 w;
-                        w.x = rc::pack_bf16(f.x, f.y);
-                        w.y = rc::pack_bf16(f.z, f.w);
-                        *reinterpret_cast<uint2*>(p.out + ((int64_t)(qo0 + tk) * p.q_heads + hh) * D + c * 32 + k8 * 4) =
-                            w;
+                    uint4* d = dst + ((int64_t)(qo0 + tk) * p.q_heads + kvh * G + cr % G) * stride + extra + c;
+                    if (whole && !p.out_wide) {  // out aligned to 8 bytes only
+                        reinterpret_cast<uint2*>(d)[0] = make_uint2(v.x, v.y);
+                        reinterpret_cast<uint2*>(d)[1] = make_uint2(v.z, v.w);
                     } else {
-                        *reinterpret_cast<float4*>(
-                            p.part_o + (((int64_t)(qo0 + tk) * p.q_heads + hh) * p.seg_chunks + chunk) * D + c * 32 +
-                            k8 * 4) = f;
+                        *d = v;
                     }
                 }
                 __syncwarp();
+            };
+            if (whole) {
+                constexpr int N = D / 8;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D / 32; ++c0) {
+                    uint32_t v[32];
+                    tc::tmem_ld32_issue(tq + 128 + c0 * 32, v);
+                    tc::tmem_ld_wait(v);
+                    auto x = [&](int i) { return __uint_as_float(v[i]) * inv; };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(stg + lane * N * 16 + (((c0 * 4 + k) ^ (lane & 7)) * 16)) =
+                            make_uint4(rc::pack_bf16(x(8 * k), x(8 * k + 1)), rc::pack_bf16(x(8 * k + 2), x(8 * k + 3)),
+                                       rc::pack_bf16(x(8 * k + 4), x(8 * k + 5)), rc::pack_bf16(x(8 * k + 6), x(8 * k + 7)));
+                }
+                write_rows(std::integral_constant<int, N>{}, reinterpret_cast<uint4*>(p.out), N, 0);
+            } else {  // fp32 partials, 32 columns (128 bytes a row) at a time
+#pragma unroll 1
+                for (int c0 = 0; c0 < D / 32; ++c0) {
+                    uint32_t v[32];
+                    tc::tmem_ld32_issue(tq + 128 + c0 * 32, v);
+                    tc::tmem_ld_wait(v);
+                    auto x = [&](int i) { return __uint_as_float(v[i]) * inv; };
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4*>(stg + lane * 128 + ((k ^ (lane & 7)) * 16)) =
+                            make_float4(x(4 * k), x(4 * k + 1), x(4 * k + 2), x(4 * k + 3));
+                    write_rows(std::integral_constant<int, 8>{}, reinterpret_cast<uint4*>(p.part_o),
+                               (int64_t)p.seg_chunks * D / 4, (int64_t)chunk * D / 4 + c0 * 8);
+                }
             }
             if (ok && row_valid) {
                 const int h = kvh * G + (row % G);
@@ -579,124 +735,24 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         // stages allow (completion is signalled on the stage's barrier by the
         // copies themselves), reading the slot ids of its next tile one tile
         // ahead.
-        // lane -> (key within an 8-key group, 16-byte column within a group of 4)
-        const int klo = lane & 7, csub = lane >> 3;
-        // keys here are shared: by the CTAs of the other row blocks, and (a
-        // cached prefix) by later steps -- keep them in L2
-        const uint64_t pol = rc::l2_policy_evict_last();
-        const int t0 = warp - 8;
-        auto load_ids = [&](int t, int (&sl)[2]) {
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-                const int key = t * TN + lane + 32 * h2;
-                sl[h2] = (t < n_tiles && key < key_count) ? __ldg(keys + key) : -1;
-            }
-        };
         if constexpr (FP4) {
-            // All producer warps widen every tile together: a stage is held from
-            // the start of its widening until P.V has read it, and one warp's
-            // ~2200 cycles for a tile were a third of that (extend 256 x
-            // (1792 + 32-64) 479 us).  Codes and scales come by cp.async into the
-            // warp's own RAW parts, two tiles ahead, and are widened from there
-            // into the operand stage.  Every value is exact in f16.
-            static_assert(NP == 3 && TN == 64, "groups of eight keys per warp");
-            constexpr int CB = D / 2, SB4 = D / 16;
-            constexpr int CPR = CB / 16;         // 16-byte chunks per row
-            constexpr int RPI = 32 / CPR;        // rows one instruction copies
-            const int wi = warp - 8;
-            const uint32_t n_slots = (uint32_t)min(p.n_slots, (int64_t)0x7fffffff);
-            unsigned char* raw = sRaw + wi * RAW * raw_bytes<D>();
-            // the tile's key of this warp's row r: groups wi, wi + NP, ...
-            auto key_of = [&](int r) { return ((r >> 3) * NP + wi) * 8 + (r & 7); };
-            // chunk c of row r lies at chunk c ^ swz(r): eight rows' equal chunks
-            // then touch every bank once
-            auto swz4 = [](int r) { return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1; };
-            // lane r: the slot id of row r's key (-1: none)
-            auto id_of = [&](int t) -> int {
-                const int key = t * TN + key_of(lane);
-                return lane < RAW_ROWS && key_of(lane) < TN && t < n_tiles && key < key_count ? __ldg(keys + key) : -1;
-            };
-            auto fetch = [&](int t, int id) {
-                if (t < n_tiles) {
-                    const uint32_t dst = rc::smem_u32(raw) + (t % RAW) * raw_bytes<D>();
-                    const int c = lane % CPR;
-                    const bool live = (uint32_t)id < n_slots;
-                    if (!live && id != -1) rc::flag_error(p.err, rc::kErrBadSlot);
-                    const int safe = live ? id : 0;
-#pragma unroll
-                    for (int i = 0; i < (RAW_ROWS + RPI - 1) / RPI; ++i) {
-                        const int r = i * RPI + lane / CPR;
-                        const int s = __shfl_sync(0xffffffffu, safe, r & 31);
-                        const int64_t off = ((int64_t)s * p.kv_heads + kvh) * CB + c * 16;
-                        const uint32_t d = dst + r * CB + ((c ^ swz4(r)) * 16);
-                        if (RAW_ROWS % RPI == 0 || r < RAW_ROWS) {
-                            rc::cp_async16(d, reinterpret_cast<const unsigned char*>(p.pool_k) + off, 16u, pol);
-                            rc::cp_async16(d + RAW_ROWS * CB, reinterpret_cast<const unsigned char*>(p.pool_v) + off, 16u,
-                                           pol);
-                        }
-                    }
-                    if (lane < RAW_ROWS) {  // zero scales: past the end, and for a slot outside the pool
-                        const int64_t off = ((int64_t)safe * p.kv_heads + kvh) * SB4;
-                        const uint32_t d = dst + 2 * RAW_ROWS * CB + lane * SB4;
-                        rc::cp_async_small<SB4>(d, p.k_bscale + off, live ? (uint32_t)SB4 : 0u);
-                        rc::cp_async_small<SB4>(d + RAW_ROWS * SB4, p.v_bscale + off, live ? (uint32_t)SB4 : 0u);
-                    }
-                }
-                rc::cp_async_commit();
-            };
-            // 32 codes under two scales per lane: eight neighbouring lanes hold
-            // eight keys' equal chunks, so a 16-byte f16 store of theirs is 128
-            // contiguous bytes
-            constexpr int KPI = 32 / (D / 32);
-            const int krow = lane & (KPI - 1), cq = lane / KPI;
-            auto widen = [&](unsigned char* dst, const unsigned char* codes, const unsigned char* scales) {
-#pragma unroll
-                for (int i = 0; i < (RAW_ROWS + KPI - 1) / KPI; ++i) {
-                    const int r = i * KPI + krow, key = key_of(r);
-                    if (r >= RAW_ROWS || key >= TN) continue;
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + r * CB + ((cq ^ swz4(r)) * 16));
-                    const uint32_t c = *reinterpret_cast<const uint16_t*>(scales + r * SB4 + 2 * cq);
-                    const uint32_t s0 = rc::scale_pair<0, 0>(c), s1 = rc::scale_pair<1, 1>(c);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // 8 codes: f16 chunk 4 cq + k
-                        uint4 f;
-                        rc::e2m1x8_to_f16x8(x[k], f.x, f.y, f.z, f.w);
-                        const uint32_t sc = k < 2 ? s0 : s1;
-                        f.x = rc::mul_f16x2(f.x, sc);
-                        f.y = rc::mul_f16x2(f.y, sc);
-                        f.z = rc::mul_f16x2(f.z, sc);
-                        f.w = rc::mul_f16x2(f.w, sc);
-                        *reinterpret_cast<uint4*>(dst + tc::cm_offset(key, 4 * cq + k, CH)) = f;
-                    }
-                }
-            };
-            int id = id_of(0), ahead;
-#pragma unroll
-            for (int i = 0; i < RAW; ++i) {
-                fetch(i, id);
-                id = id_of(i + 1);
-            }
             int s = 0, ph = 1;  // stage, and the parity of the wait for it (its first use waits for nothing)
             for (int t = 0; t < n_tiles && ok; ++t) {
-                ahead = id_of(t + RAW + 1);
+                const int ahead = feed.id_of(t + RAW + 1);
                 if (t >= NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], ph, kWaitIter));
                 if (!ok) break;
                 rc::cp_async_wait<RAW - 1>();
                 __syncwarp();
-                const unsigned char* src = raw + (t % RAW) * raw_bytes<D>();
-                unsigned char* dst = sKV + s * 2 * KV_BYTES;
-                widen(dst, src, src + 2 * RAW_ROWS * CB);
-                widen(dst + KV_BYTES, src + RAW_ROWS * CB, src + 2 * RAW_ROWS * CB + RAW_ROWS * SB4);
+                feed.put(t, sKV + s * 2 * KV_BYTES);
                 tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
                 mbar_arrive(&kv_full[s]);
                 __syncwarp();  // every lane has read the raw tile
-                fetch(t + RAW, id);
-                id = ahead;
+                feed.fetch(t + RAW, feed_id);
+                feed_id = ahead;
                 if (++s == NS) s = 0, ph ^= 1;
             }
         }
-        int sl[2] = {sl_first[0], sl_first[1]}, sl_next[2];
+        int sl_next[2];
         for (int t = FP4 ? n_tiles : t0; t < n_tiles && ok; t += NP) {
             const int s = t % NS;
             load_ids(t + NP, sl_next);
@@ -705,6 +761,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             unsigned char* sK = sKV + s * 2 * KV_BYTES;
             unsigned char* sV = sK + KV_BYTES;
             if constexpr (FP8) {
+                const int klo = lane & 7, csub = lane >> 3;
                 // 16 E4M3 codes per load (8 keys x 64 bytes per instruction,
                 // so the 16-byte f16 stores of 8 keys are 128 contiguous bytes);
                 // the K and V loads of the tile are all in flight together
@@ -763,25 +820,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                 mbar_arrive(&kv_full[s]);
             }
             if constexpr (!F16) {
-#pragma unroll
-                for (int kg = 0; kg < TN / 8; ++kg) {
-                    const int key = kg * 8 + klo;
-                    int slot = __shfl_sync(0xffffffffu, sl[kg >> 2], (kg & 3) * 8 + klo);
-                    uint32_t bytes = 16;
-                    if (t * TN + key >= key_count) { slot = 0; bytes = 0; }
-                    else if (slot < 0 || (int64_t)slot >= p.n_slots) {
-                        rc::flag_error(p.err, rc::kErrBadSlot);
-                        slot = 0;
-                        bytes = 0;
-                    }
-                    // chunks c = 4 cg + csub: 512 bytes apart in the stage, 64 in the row
-                    const int64_t base = ((int64_t)slot * p.kv_heads + kvh) * D + csub * 8;
-                    const uint32_t off = tc::cm_offset(key, csub, CH);
-                    rc::cp_async16_run<512, 64>(rc::smem_u32(sK) + off, p.pool_k + base, bytes, pol,
-                                                std::make_integer_sequence<int, CH / 4>{});
-                    rc::cp_async16_run<512, 64>(rc::smem_u32(sV) + off, p.pool_v + base, bytes, pol,
-                                                std::make_integer_sequence<int, CH / 4>{});
-                }
+                if (t > t0) copy_tile(t, sl);  // (the first went out before the set-up)
                 // each lane arrives on the stage's barrier when its copies have
                 // landed; the warp goes on to the next tile at once
                 tc::cp_async_mbar_arrive(&kv_full[s]);

@@ -26,6 +26,7 @@ struct MQParams {
     int64_t table_len;
     __nv_bfloat16* out;
     float* lse;
+    int32_t out_wide;  // out is 16-byte aligned
     // cascade: rows are the requests sharing segment blockIdx.z
     const int32_t* seg_slots;
     const int32_t* seg_indptr;
