@@ -573,18 +573,21 @@ def make_rope_desc(cos_sin, interleaved: bool = False, offset: int = 0) -> rc_ro
 def _rows(name, t, n, heads, dim, bf16, write=False):
     """Stride between tokens of bf16 rows [n, heads, dim], each token's rows
     dense; tokens may be further apart (a slice of a projection's output)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [{n}, {heads}, {dim}], got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if n <= 1:
+        s0 = heads * dim
+    if t.shape == (n, heads, dim) and t.dtype is bf16 and s2 == 1 and (s1 == dim or heads == 1) and \
+            not (write and s0 < heads * dim):
+        return s0
     if t.shape != (n, heads, dim):
         raise ValueError(f"{name}: expected [{n}, {heads}, {dim}], got {tuple(t.shape)}")
     if t.dtype is not bf16:
         raise ValueError(f"{name}: expected bf16, got {t.dtype}")
-    s0, s1, s2 = t.stride()
-    if n <= 1:
-        s0 = heads * dim
-    if s2 != 1 or (s1 != dim and heads > 1):
-        raise ValueError(f"{name}: each token's rows must be dense, got strides {t.stride()}")
-    if write and s0 < heads * dim:
+    if write and s0 < heads * dim and s2 == 1:
         raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
-    return s0
+    raise ValueError(f"{name}: each token's rows must be dense, got strides {t.stride()}")
 
 
 def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_new, v_new, q=None, q_out=None,

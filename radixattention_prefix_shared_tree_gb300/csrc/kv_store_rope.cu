@@ -106,7 +106,7 @@ RC_DEV uint2 e4m3_codes(const float (&x)[8], float scale) {
 
 // U: units per head row (D / 16).  ROT 0: no rotation; 1: pairs half the
 // rotated width apart; 2: neighbouring pairs.
-template <int U, int FMT, int ROT>
+template <int U, int FMT, int ROT, int UN>
 __global__ void __launch_bounds__(256) store_rope_kernel(const StoreParams p) {
     constexpr int D = 16 * U, CH = 2 * U;
     constexpr bool FIXED = 32 % U == 0;  // a lane's unit is the same in every row
@@ -173,6 +173,13 @@ __global__ void __launch_bounds__(256) store_rope_kernel(const StoreParams p) {
         b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
         a = x;
     };
+    // what unit e of the token is: its row's source and head, its chunks, whether
+    // they turn, and whether they are read at all
+    struct Unit {
+        const uint4* src;
+        int head, u, c0, c1;
+        bool live, is_k, is_q, r0, r1, t0, t1;
+    };
     int fc0 = 0, fc1 = 0;
     bool fr0 = false, fr1 = false;
     if constexpr (FIXED) {
@@ -180,87 +187,105 @@ __global__ void __launch_bounds__(256) store_rope_kernel(const StoreParams p) {
         if constexpr (ROT != 0) load_angles(lane % U, fc0, fc1, fr0, fr1);
     }
 
-    for (int e0 = begin; e0 < end; e0 += 32) {
-        const int e = e0 + lane;
-        const bool live = e < end;
-        const int row = e / U, u = FIXED ? lane % U : e - row * U;
-        int c0 = fc0, c1 = fc1;
-        bool r0 = fr0, r1 = fr1;
-        if constexpr (!FIXED) chunks(u, c0, c1, r0, r1);
-        const bool is_k = row < k_rows, is_q = row >= k_rows + v_rows;
-        const int head = is_k ? row : is_q ? row - k_rows - v_rows : row - k_rows;
-        if (!is_k && !is_q) r0 = r1 = false;  // V is stored as it is
-        const __nv_bfloat16* src = is_q ? p.q + (int64_t)t * p.q_stride
-                                        : is_k ? p.k + (int64_t)t * p.k_stride : p.v + (int64_t)t * p.v_stride;
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + (int64_t)head * D);
-        const bool keep = is_q && in_place;  // columns that stay as they are need no copy
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const bool t0 = live && !(keep && !r0), t1 = live && !(keep && !r1);
-        uint4 w0 = t0 ? s4[c0] : z, w1 = t1 ? s4[c1] : z;
-        float x0[8], x1[8];
-        if constexpr (ROT != 0 || FMT != rc::kFmtBf16) {
-            unpack(w0, x0);
-            unpack(w1, x1);
-            if constexpr (ROT != 0 && !FIXED)
-                if (r0 || r1) load_angles(u, c0, c1, r0, r1);
-            if constexpr (ROT == 1) {
-                if (r0) {
+    auto unit = [&](int e) -> Unit {
+        Unit m;
+        m.live = e < end;
+        const int row = e / U;
+        m.u = FIXED ? lane % U : e - row * U;
+        m.c0 = fc0, m.c1 = fc1, m.r0 = fr0, m.r1 = fr1;
+        if constexpr (!FIXED) chunks(m.u, m.c0, m.c1, m.r0, m.r1);
+        m.is_k = row < k_rows;
+        m.is_q = row >= k_rows + v_rows;
+        m.head = m.is_k ? row : m.is_q ? row - k_rows - v_rows : row - k_rows;
+        if (!m.is_k && !m.is_q) m.r0 = m.r1 = false;  // V is stored as it is
+        const __nv_bfloat16* s = m.is_q ? p.q + (int64_t)t * p.q_stride
+                                        : m.is_k ? p.k + (int64_t)t * p.k_stride : p.v + (int64_t)t * p.v_stride;
+        m.src = reinterpret_cast<const uint4*>(s + (int64_t)m.head * D);
+        const bool keep = m.is_q && in_place;  // columns that stay as they are need no copy
+        m.t0 = m.live && !(keep && !m.r0);
+        m.t1 = m.live && !(keep && !m.r1);
+        return m;
+    };
+
+    // UN units per lane at a time, all their loads before the first is used
+    for (int e0 = begin; e0 < end; e0 += 32 * UN) {
+        uint4 w0[UN], w1[UN];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) turn(x0[i], x1[i], cs[i], sn[i]);
-                }
-            }
-            if constexpr (ROT == 2) {
-                if (r0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) turn(x0[2 * i], x0[2 * i + 1], cs[i], sn[i]);
-                }
-                if (r1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) turn(x1[2 * i], x1[2 * i + 1], cs[4 + i], sn[4 + i]);
-                }
-            }
-            if (r0) w0 = pack(x0);
-            if (r1) w1 = pack(x1);
+        for (int i = 0; i < UN; ++i) {
+            const Unit m = unit(e0 + 32 * i + lane);
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            w0[i] = m.t0 ? m.src[m.c0] : z;
+            w1[i] = m.t1 ? m.src[m.c1] : z;
         }
-        if (is_q) {
-            uint4* d4 = reinterpret_cast<uint4*>(p.q_out + (int64_t)t * p.q_out_stride + (int64_t)head * D);
-            if (t0) d4[c0] = w0;
-            if (t1) d4[c1] = w1;
-        }
-        const bool put = live && !is_q && slot_ok;
-        const int64_t prow = (int64_t)(slot_ok ? slot : 0) * p.kv_heads + head;
-        if constexpr (FMT == rc::kFmtBf16) {
-            uint4* d4 = reinterpret_cast<uint4*>(is_k ? p.pool_k : p.pool_v) + prow * CH;
-            if (put) {
-                d4[c0] = w0;
-                d4[c1] = w1;
-            }
-        } else if constexpr (FMT == rc::kFmtFp8) {  // 8 lanes hold a row
-            float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
+        for (int i = 0; i < UN; ++i) {
+            if (e0 + 32 * i >= end) break;  // (uniform)
+            const Unit m = unit(e0 + 32 * i + lane);
+            float x0[8], x1[8];
+            if constexpr (ROT != 0 || FMT != rc::kFmtBf16) {
+                unpack(w0[i], x0);
+                unpack(w1[i], x1);
+                if constexpr (ROT != 0 && !FIXED)
+                    if (m.r0 || m.r1) load_angles(m.u, m.c0, m.c1, m.r0, m.r1);
+                if constexpr (ROT == 1) {
+                    if (m.r0) {
 #pragma unroll
-            for (int i = 1; i < U; i <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, i));
-            const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
-            if (put) {
-                uint2* d2 = reinterpret_cast<uint2*>(is_k ? p.pool_k : p.pool_v) + prow * CH;
-                d2[c0] = e4m3_codes(x0, scale);
-                d2[c1] = e4m3_codes(x1, scale);
-                if (u == 0) (is_k ? p.k_scale : p.v_scale)[prow] = scale;
+                        for (int j = 0; j < 8; ++j) turn(x0[j], x1[j], cs[j], sn[j]);
+                    }
+                }
+                if constexpr (ROT == 2) {
+                    if (m.r0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) turn(x0[2 * j], x0[2 * j + 1], cs[j], sn[j]);
+                    }
+                    if (m.r1) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) turn(x1[2 * j], x1[2 * j + 1], cs[4 + j], sn[4 + j]);
+                    }
+                }
+                if (m.r0) w0[i] = pack(x0);
+                if (m.r1) w1[i] = pack(x1);
             }
-        } else {  // a block of 16 is the chunk of this lane and the next: chunks 2i and 2i + 1
-            uint32_t a0 = abs_bits_max(x0), a1 = abs_bits_max(x1);
-            a0 = max(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-            a1 = max(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-            if (put) {
-                const uint32_t b0 = block_scale(a0), b1 = block_scale(a1);
-                uint32_t* d1 = reinterpret_cast<uint32_t*>(is_k ? p.pool_k : p.pool_v) + prow * CH;
-                d1[c0] = e2m1_codes(x0, b0);
-                d1[c1] = e2m1_codes(x1, b1);
-                if (!(lane & 1)) {
-                    uint8_t* bs = (is_k ? p.k_bscale : p.v_bscale) + prow * U;
-                    bs[c0 / 2] = (uint8_t)b0;
-                    bs[c1 / 2] = (uint8_t)b1;
+            if (m.is_q) {
+                uint4* d4 = reinterpret_cast<uint4*>(p.q_out + (int64_t)t * p.q_out_stride + (int64_t)m.head * D);
+                if (m.t0) d4[m.c0] = w0[i];
+                if (m.t1) d4[m.c1] = w1[i];
+            }
+            const bool put = m.live && !m.is_q && slot_ok;
+            const int64_t prow = (int64_t)(slot_ok ? slot : 0) * p.kv_heads + m.head;
+            if constexpr (FMT == rc::kFmtBf16) {
+                uint4* d4 = reinterpret_cast<uint4*>(m.is_k ? p.pool_k : p.pool_v) + prow * CH;
+                if (put) {
+                    d4[m.c0] = w0[i];
+                    d4[m.c1] = w1[i];
+                }
+            } else if constexpr (FMT == rc::kFmtFp8) {  // 8 lanes hold a row
+                float amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(x0[j]), fabsf(x1[j])));
+#pragma unroll
+                for (int j = 1; j < U; j <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, j));
+                const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
+                if (put) {
+                    uint2* d2 = reinterpret_cast<uint2*>(m.is_k ? p.pool_k : p.pool_v) + prow * CH;
+                    d2[m.c0] = e4m3_codes(x0, scale);
+                    d2[m.c1] = e4m3_codes(x1, scale);
+                    if (m.u == 0) (m.is_k ? p.k_scale : p.v_scale)[prow] = scale;
+                }
+            } else {  // a block of 16 is the chunk of this lane and the next: chunks 2i and 2i + 1
+                uint32_t a0 = abs_bits_max(x0), a1 = abs_bits_max(x1);
+                a0 = max(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+                a1 = max(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+                if (put) {
+                    const uint32_t b0 = block_scale(a0), b1 = block_scale(a1);
+                    uint32_t* d1 = reinterpret_cast<uint32_t*>(m.is_k ? p.pool_k : p.pool_v) + prow * CH;
+                    d1[m.c0] = e2m1_codes(x0, b0);
+                    d1[m.c1] = e2m1_codes(x1, b1);
+                    if (!(lane & 1)) {
+                        uint8_t* bs = (m.is_k ? p.k_bscale : p.v_bscale) + prow * U;
+                        bs[m.c0 / 2] = (uint8_t)b0;
+                        bs[m.c1 / 2] = (uint8_t)b1;
+                    }
                 }
             }
         }
@@ -271,16 +296,19 @@ template <int U, int FMT, int ROT>
 rc_status launch(StoreParams& p, cudaStream_t st) {
     const int units = (p.kv_heads * (p.v ? 2 : 1) + (p.q ? p.q_heads : 0)) * U;
     // A warp takes one 32-unit pass of its token while that keeps the grid
-    // within a few waves; beyond, four passes, which share the token's angles.
+    // within a few waves; beyond, kPasses, which share the token's angles and
+    // whose loads are all on their way together.
+    constexpr int kPasses = 4;
     const int64_t passes = (units + 31) / 32;
     const int64_t few = (int64_t)rc_host::sm_count() * 64;
-    const int per = (int64_t)p.n * passes <= few ? 1 : 4;
-    p.per_slice = 32 * per;
+    const bool many = (int64_t)p.n * passes > few;
+    p.per_slice = 32 * (many ? kPasses : 1);
     p.slices = (units + p.per_slice - 1) / p.per_slice;
     const int64_t warps = (int64_t)p.n * p.slices;
     const int64_t blocks = (warps + 7) / 8;
     if (blocks > 0x7fffffff) return RC_ERR_ARG;
-    store_rope_kernel<U, FMT, ROT><<<(unsigned)blocks, 256, 0, st>>>(p);
+    if (many) store_rope_kernel<U, FMT, ROT, kPasses><<<(unsigned)blocks, 256, 0, st>>>(p);
+    else store_rope_kernel<U, FMT, ROT, 1><<<(unsigned)blocks, 256, 0, st>>>(p);
     return rc_host::launch_status(cudaGetLastError());
 }
 
