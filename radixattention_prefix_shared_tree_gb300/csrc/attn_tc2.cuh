@@ -393,15 +393,36 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             return;
         }
     }
-    // a wait gave up in an earlier CTA: the results are void, leave at once,
-    // all threads alike (the word can change between two threads' reads, and
-    // a CTA split here would stall at its first barrier)
-    if (__syncthreads_or(p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout))) return;
+    // a wait gave up in an earlier CTA: the results are void (looked at at the
+    // set-up barrier)
+    const int gave_up = p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout);
     const int n_tiles = (key_count + TN - 1) / TN;
     // query tiles with at least one valid row
     const int n_qt = min(QT, ((min(n_rows_tok - tok0, TPC) * G) + TM - 1) / TM);
 
-    // Producers: their first tiles' copies go out before the set-up, which
+    // set-up by the MMA warp, which has no loads of its own on their way (the
+    // fence would wait for them)
+    if (warp == MMA_WARP) {
+        if (lane == 0) {
+            tc::mbar_init(q_full, 8);
+            for (int s = 0; s < NS; ++s) {
+                tc::mbar_init(&kv_full[s], FP4 ? 32 * NP : 32);
+                tc::mbar_init(&kv_empty[s], 1);
+            }
+            for (int i = 0; i < 4; ++i) {
+                tc::mbar_init(&s_full[i], 1);
+                tc::mbar_init(&p_full[i], 4);
+            }
+            for (int q = 0; q < QT; ++q) {
+                tc::mbar_init(&o_done[q], 1);
+            }
+            tc::fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc(tslot, 512);
+        tc::tmem_relinquish();
+    }
+    // Producers: their first tiles' copies go out before the set-up barrier, which
     // their latency then overlaps (a stage's first use waits for nothing).
     // Keys here are shared: by the CTAs of the other row blocks, and (a cached
     // prefix) by later steps -- keep them in L2.
@@ -456,6 +477,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                 if (t0 < n_tiles) copy_tile(t0, sl);
         }
     }
+    uint4 qv[F16 ? CH : 1];
     if (warp < 8) {
         // Q rows of query tile warp/4, issued first so that their latency
         // overlaps the set-up.  The row indices (cascade: a gather through
@@ -476,21 +498,11 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             else qrow[i] = qok[i] ? (int64_t)__ldg(p.seg_rows + qo0 + tk) * p.q_heads + h : 0;
             if (!qok[i]) qrow[i] = 0;
         }
-        if constexpr (F16) {  // f16 operand: load, convert, store
-            uint4 qv[CH];
+        if constexpr (F16) {  // f16 operand: loaded here, converted and stored after the barrier
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int c = ((r + 128 * i) >> 3) % CH;
                 qv[i] = qok[i] ? __ldg(reinterpret_cast<const uint4*>(p.q + qrow[i] * D + c * 8)) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int gi = r + 128 * i;
-                const int rr = (gi & 7) + 8 * (gi / (8 * CH));
-                const int c = (gi >> 3) % CH;
-                *reinterpret_cast<uint4*>(sQq + tc::cm_offset(rr, c, CH)) =
-                    make_uint4(rc::bf16x2_to_f16x2(qv[i].x), rc::bf16x2_to_f16x2(qv[i].y),
-                               rc::bf16x2_to_f16x2(qv[i].z), rc::bf16x2_to_f16x2(qv[i].w));
             }
         } else {
 #pragma unroll
@@ -504,29 +516,16 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             rc::cp_async_commit();
         }
     }
-    if (tid == 0) {
-        tc::mbar_init(q_full, 8);
-        for (int s = 0; s < NS; ++s) {
-            tc::mbar_init(&kv_full[s], FP4 ? 32 * NP : 32);
-            tc::mbar_init(&kv_empty[s], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&s_full[i], 1);
-            tc::mbar_init(&p_full[i], 4);
-        }
-        for (int q = 0; q < QT; ++q) {
-            tc::mbar_init(&o_done[q], 1);
-        }
-        tc::fence_mbar_init();
-    }
-    if (warp == MMA_WARP) {
-        tc::tmem_alloc(tslot, 512);
-        tc::tmem_relinquish();
-    }
     tc::fence_before();
-    __syncthreads();
+    const int leave = __syncthreads_or(gave_up);
     tc::fence_after();
     const uint32_t tbase = *tslot;
+    if (leave) {  // all threads alike (the word can change between two threads' reads)
+        rc::cp_async_wait<0>();
+        __syncthreads();
+        if (warp == MMA_WARP) tc::tmem_dealloc(tbase, 512);
+        return;
+    }
     bool ok = true;
 
     if (warp < 8) {
@@ -536,6 +535,18 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         const int row = q * TM + r;          // row within the CTA
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tq = tbase + q * 256 + lane_off;
+        if constexpr (F16) {
+            unsigned char* sQq = sQ + q * TM * D * 2;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int gi = r + 128 * i;
+                const int rr = (gi & 7) + 8 * (gi / (8 * CH));
+                const int c = (gi >> 3) % CH;
+                *reinterpret_cast<uint4*>(sQq + tc::cm_offset(rr, c, CH)) =
+                    make_uint4(rc::bf16x2_to_f16x2(qv[i].x), rc::bf16x2_to_f16x2(qv[i].y),
+                               rc::bf16x2_to_f16x2(qv[i].z), rc::bf16x2_to_f16x2(qv[i].w));
+            }
+        }
         rc::cp_async_wait<0>();  // this thread's Q chunks (issued before the set-up)
         tc::fence_proxy_async();
         __syncwarp();
