@@ -64,6 +64,11 @@ inline int groups(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t sms)
     const int64_t g = resident < most ? resident : most;
     return (int)(g < 1 ? 1 : g);
 }
+// The runs of a batch of so many tiles, given the most there may be.
+RC_DEV int64_t runs_of(int64_t tiles, int most) {
+    const int64_t r = (tiles + kMinTiles - 1) / kMinTiles;
+    return r < most ? r : most;
+}
 // One warp per (row, KV head) and no merge: rows short enough, and enough of
 // them, that a warp each fills most of the SMs.
 inline bool whole_rows(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t sms) {
@@ -149,8 +154,7 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         }
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, k);
-        int64_t runs = (tiles + kMinTiles - 1) / kMinTiles;
-        runs = runs < p.n_chunks ? runs : p.n_chunks;
+        const int64_t runs = runs_of(tiles, p.n_chunks);
         if (group >= runs) {
             grid_dep_wait();
             return;
@@ -495,16 +499,37 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
     const RowKeys r = row_keys<CROSS>(p, b);
     const int s0 = !CROSS && p.req_seg_indptr ? p.req_seg_indptr[b] : 0;
     int n_seg = !CROSS && p.req_seg_indptr ? (p.req_seg_indptr[b + 1] - s0) * p.seg_chunks : 0;
+    // The runs that touch the row: up to 32 rows from the lengths, ahead of the
+    // wait; beyond, as the split pass noted them.
+    int g0 = 0, g1 = -1;
+    if (p.batch <= 32) {
+        const int n = (row_keys<CROSS>(p, lane).L + fp4::kKeys - 1) / fp4::kKeys;
+        int64_t incl = n;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
+            if (lane >= k) incl += v;
+        }
+        const int64_t tiles = __shfl_sync(0xffffffffu, incl, 31), end = __shfl_sync(0xffffffffu, incl, b);
+        const int64_t first = end - __shfl_sync(0xffffffffu, n, b), runs = fp4::runs_of(tiles, p.n_chunks);
+        if (r.L > 0) {  // run g begins at tile g * tiles / runs: tile x lies in the last that begins by x
+            g0 = (int)(((first + 1) * runs - 1) / tiles);
+            g1 = (int)((end * runs - 1) / tiles);
+        }
+    }
     grid_dep_wait();
     const bool live = h < p.q_heads && (!CROSS || token * p.group < r.ncol);
     if (W == 1 && !live) return;
     // a cascade kernel that gave up on a bounded wait left its partials unwritten
     if (n_seg && p.err && (*reinterpret_cast<volatile int32_t*>(p.err) & rc::kErrTimeout)) n_seg = 0;
-    const int g0 = r.L > 0 ? p.row_runs[2 * b] : 0, g1 = r.L > 0 ? p.row_runs[2 * b + 1] : -1;
+    if (p.batch > 32 && r.L > 0) g0 = p.row_runs[2 * b], g1 = p.row_runs[2 * b + 1];
     const int n_all = live ? n_seg + g1 - g0 + 1 : 0;
     const int kvh = h / p.group, nc = CROSS ? 8 : p.group, col = token * p.group + h % p.group;
-    // lane l looks up the l-th of a round of 32 and its log-sum-exp, then all
-    // lanes read the rows (independent loads), against a running maximum
+    // lane l looks up the l-th of a round of 32 and its log-sum-exp; all lanes
+    // read the rows, eight at a time, the first eight while the log-sum-exps
+    // are still on their way (a segment chunk without keys has an unwritten
+    // row and no weight); against a running maximum
+    constexpr int R = 8;
     float m = -INFINITY, wsum = 0.f, acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
@@ -518,6 +543,17 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
             row = ((int64_t)(g0 + b + j - n_seg) * p.kv_heads + kvh) * nc + col;
         const float l2 = j < n_all ? (in_seg ? p.seg_lse : p.part_lse)[row] : -INFINITY;
         const float* src = (in_seg ? p.seg_o : p.part_o) + row * D;
+        const int nb = min(32, (n_all - j0 + W - 1) / W);
+        Vec v[R];
+        auto read = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float* s = reinterpret_cast<const float*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), min(i0 + i, nb - 1)));
+                if (i0 + i < nb) v[i] = reinterpret_cast<const Vec*>(s)[lane];
+            }
+        };
+        read(0);
         float mb = fmaxf(m, l2);
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, k));
@@ -528,16 +564,14 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
         for (int k = 0; k < V; ++k) acc[k] *= a;
         m = mb;
         const float wt = l2 == -INFINITY ? 0.f : rc::fast_exp2(l2 - m);
-        const int nb = min(32, (n_all - j0 + W - 1) / W);
-#pragma unroll 8
-        for (int i = 0; i < nb; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wt, i);
-            const float* s = reinterpret_cast<const float*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
-            wsum += wi;
-            if (wi != 0.f) {  // a partial without keys is not written
-                const Vec v = reinterpret_cast<const Vec*>(s)[lane];
-                const float* x = reinterpret_cast<const float*>(&v);
+        for (int i0 = 0; i0 < nb; i0 += R) {
+            if (i0 > 0) read(i0);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float wi = i0 + i < nb ? __shfl_sync(0xffffffffu, wt, i0 + i) : 0.f;
+                if (wi == 0.f) continue;
+                wsum += wi;
+                const float* x = reinterpret_cast<const float*>(&v[i]);
 #pragma unroll
                 for (int k = 0; k < V; ++k) acc[k] += wi * x[k];
             }

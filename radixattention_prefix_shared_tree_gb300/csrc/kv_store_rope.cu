@@ -18,6 +18,8 @@
 
 namespace {
 
+constexpr int kWarps = 4;  // per block
+
 struct StoreParams {
     const __nv_bfloat16* k;
     const __nv_bfloat16* v;   // NULL: latent pool
@@ -107,7 +109,7 @@ RC_DEV uint2 e4m3_codes(const float (&x)[8], float scale) {
 // U: units per head row (D / 16).  ROT 0: no rotation; 1: pairs half the
 // rotated width apart; 2: neighbouring pairs.
 template <int U, int FMT, int ROT, int UN>
-__global__ void __launch_bounds__(256) store_rope_kernel(const StoreParams p) {
+__global__ void __launch_bounds__(32 * kWarps) store_rope_kernel(const StoreParams p) {
     constexpr int D = 16 * U, CH = 2 * U;
     constexpr bool FIXED = 32 % U == 0;  // a lane's unit is the same in every row
     const int lane = threadIdx.x & 31;
@@ -296,19 +298,22 @@ template <int U, int FMT, int ROT>
 rc_status launch(StoreParams& p, cudaStream_t st) {
     const int units = (p.kv_heads * (p.v ? 2 : 1) + (p.q ? p.q_heads : 0)) * U;
     // A warp takes one 32-unit pass of its token while that keeps the grid
-    // within a few waves; beyond, kPasses, which share the token's angles and
-    // whose loads are all on their way together.
-    constexpr int kPasses = 4;
-    const int64_t passes = (units + 31) / 32;
+    // within a few waves; beyond, up to kPasses, which share the token's angles
+    // and whose loads are all on their way together.  (14,001 tokens of 48 rows of
+    // 128: 3 passes 65 us, 4 64, 6 59, 8 72; 1,023 latent tokens: 3 62, 4 55,
+    // 6 57.  256 threads a block instead of 128: 67 and 57.)
+    constexpr int kPasses = U == 36 ? 4 : 6;
+    const int passes = (units + 31) / 32;
     const int64_t few = (int64_t)rc_host::sm_count() * 64;
     const bool many = (int64_t)p.n * passes > few;
-    p.per_slice = 32 * (many ? kPasses : 1);
+    const int cut = (passes + kPasses - 1) / kPasses;  // warps per token, of as many passes each as any other
+    p.per_slice = 32 * (many ? (passes + cut - 1) / cut : 1);
     p.slices = (units + p.per_slice - 1) / p.per_slice;
     const int64_t warps = (int64_t)p.n * p.slices;
-    const int64_t blocks = (warps + 7) / 8;
+    const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return RC_ERR_ARG;
-    if (many) store_rope_kernel<U, FMT, ROT, kPasses><<<(unsigned)blocks, 256, 0, st>>>(p);
-    else store_rope_kernel<U, FMT, ROT, 1><<<(unsigned)blocks, 256, 0, st>>>(p);
+    if (many) store_rope_kernel<U, FMT, ROT, kPasses><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(p);
+    else store_rope_kernel<U, FMT, ROT, 1><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(p);
     return rc_host::launch_status(cudaGetLastError());
 }
 
