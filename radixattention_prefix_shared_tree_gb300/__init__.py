@@ -570,58 +570,40 @@ def make_rope_desc(cos_sin, interleaved: bool = False, offset: int = 0) -> rc_ro
     return r
 
 
-def _rows(name, t, n, heads, dim, bf16, write=False):
-    """Stride between tokens of bf16 rows [n, heads, dim], each token's rows
-    dense; tokens may be further apart (a slice of a projection's output)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [{n}, {heads}, {dim}], got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if n <= 1:
-        s0 = heads * dim
-    if t.shape == (n, heads, dim) and t.dtype is bf16 and s2 == 1 and (s1 == dim or heads == 1) and \
-            not (write and s0 < heads * dim):
-        return s0
-    if t.shape != (n, heads, dim):
-        raise ValueError(f"{name}: expected [{n}, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.dtype is not bf16:
-        raise ValueError(f"{name}: expected bf16, got {t.dtype}")
-    if write and s0 < heads * dim and s2 == 1:
-        raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
-    raise ValueError(f"{name}: each token's rows must be dense, got strides {t.stride()}")
+_host_call = None
+
+
+def _host_store_rope():
+    """kv_store_rope of the marshalling module (csrc/host_binding.c): checks
+    the tensors and calls the library, several times faster than ctypes."""
+    global _host_call
+    if _host_call is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch
+        path = _build.HOST
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first (python -m radixattention_prefix_shared_tree_gb300._compile)")
+        loader = importlib.machinery.ExtensionFileLoader("radixattn_host", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("radixattn_host", loader))
+        loader.exec_module(mod)
+        mod.bind(C.cast(lib().kv_store_rope, VP).value, torch.bfloat16, torch.int32, torch._C._cuda_getDevice,
+                 torch._C._cuda_getCurrentRawStream)
+        _host_call = mod.kv_store_rope
+    return _host_call
 
 
 def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_new, v_new, q=None, q_out=None,
                   table=None, table_pos=None, stream=None):
     """Append n tokens with K (and Q) rotated by their positions (see the
-    header).  k_new, v_new [n, Hkv, d], q, q_out [n, Hq, d]: bf16, token strides
-    of their own; v_new None for a latent pool; q_out None rotates q in place.
-    slots, positions: int32 [n]."""
-    import torch
-    bf16 = torch.bfloat16
-    n, hkv, d = slots.numel(), pool.kv_heads, pool.head_dim_k
-    if positions.numel() != n or slots.dtype is not torch.int32 or positions.dtype is not torch.int32:
-        raise ValueError("kv_store_rope: slots and positions are int32 of one length")
-    ks = _rows("k_new", k_new, n, hkv, d, bf16)
-    vs = _rows("v_new", v_new, n, hkv, d, bf16) if v_new is not None else 0
-    hq = qs = os_ = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError(f"q: expected [{n}, heads, {d}], got {tuple(q.shape)}")
-        hq = q.shape[1]
-        qs = _rows("q", q, n, hq, d, bf16, q_out is None)
-        if q_out is None:
-            q_out, os_ = q, qs
-        else:
-            os_ = _rows("q_out", q_out, n, hq, d, bf16, True)
-    elif q_out is not None:
-        raise ValueError("kv_store_rope: q_out without q")
-    _on_device("kv_store_rope", slots, positions, k_new, v_new, q, q_out, table, table_pos)
-    st = lib().kv_store_rope(C.byref(pool), C.byref(rope), _ptr(slots), _ptr(positions), k_new.data_ptr(), ks,
-                             v_new.data_ptr() if v_new is not None else None, vs, n,
-                             q.data_ptr() if hq else None, qs, hq, q_out.data_ptr() if hq else None, os_,
-                             _ptr(table), _ptr(table_pos),
-                             _stream(stream))
-    _check("kv_store_rope", st)
+    header).  k_new, v_new [n, Hkv, d], q, q_out [n, Hq, d]: bf16, each token's
+    rows dense, tokens any distance apart; v_new None for a latent pool; q_out
+    None rotates q in place.  slots, positions, table_pos: int32 [n]."""
+    st = (_host_call or _host_store_rope())(C.addressof(pool), C.addressof(rope), slots, positions, k_new, v_new, q, q_out,
+                                            table, table_pos, stream)
+    if st:
+        _check("kv_store_rope", st)
 
 
 def attn_decode_workspace(desc: rc_attn_desc, batch: int, max_len: int, cascade: rc_cascade | None = None) -> int:

@@ -1,5 +1,8 @@
 """Build the C-ABI library ``_build/libradixattn.so`` in-tree with nvcc (sm_103a).
 
+Beside it goes ``_build/radixattn_host.so``, the Python module that marshals
+kv_store_rope's tensors (plain C, no torch headers).
+
 Translation units compile in parallel; the host tree is plain C++ (g++), the
 kernels are CUDA for ``arch=compute_103a,code=sm_103a``.  cudart is linked
 statically so the library does not depend on which libcudart the process
@@ -10,11 +13,13 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libradixattn.so")
+HOST = os.path.join(BUILD, "radixattn_host.so")   # argument marshalling for Python (csrc/host_binding.c)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 CU_SOURCES = ["kv_store.cu", "kv_store_rope.cu", "attn_decode.cu", "attn_decode_mla.cu", "attn_extend.cu", "attn_cross.cu",
@@ -38,9 +43,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(HOST)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -62,6 +67,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = ["g++", "-O3", "-std=c++17", "-fPIC", "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj]
         jobs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    host_tmp = HOST + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "host_binding.c"), "-o", host_tmp]
+    jobs.append(("host_binding.c", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in jobs:
         out, _ = pr.communicate()
@@ -74,6 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nv] + ARCH + ["-shared", "-o", tmp] + objs + ["-lstdc++"])
     os.replace(tmp, LIB)
+    os.replace(host_tmp, HOST)
     return LIB
 
 

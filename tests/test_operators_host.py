@@ -103,7 +103,7 @@ def test_kv_store_rope_refusals(built):
     assert call_rope(fp4_pool(d=256), rope_desc(), d=256) == U
 
 
-def test_kv_store_rope_binding_checks_shapes():
+def test_kv_store_rope_binding_checks_shapes(built):
     pool, r = bf16_pool(), rope_desc()
     k = torch.zeros(4, 8, 128, dtype=BF)
     q = torch.zeros(4, 32, 128, dtype=BF)
@@ -112,12 +112,15 @@ def test_kv_store_rope_binding_checks_shapes():
     good = dict(slots=slots, positions=slots, k_new=k, v_new=k, q=q, q_out=torch.zeros_like(q))
     bad = [dict(k_new=k[:3]), dict(k_new=k.float()), dict(k_new=k[:, :4]), dict(v_new=k[..., :64]),
            dict(k_new=k.transpose(1, 2)), dict(q_out=q[:, :16].contiguous()), dict(positions=slots[:3]),
-           dict(slots=slots.long()), dict(q_out=torch.zeros(1, 32, 128, dtype=BF).expand(4, 32, 128)),
+           dict(slots=slots.long()), dict(slots=slots[None]), dict(table=slots.float()), dict(table_pos=slots[:3]),
+           dict(positions=slots.repeat_interleave(2)[::2]), dict(q=None), dict(q=q[0], q_out=None), dict(q=q[:, :0], q_out=q[:, :0]), dict(q_out=torch.zeros(1, 32, 128, dtype=BF).expand(4, 32, 128)),
            dict(k_new=torch.zeros(4, 128, 8, dtype=BF).transpose(1, 2))]
     for kw in bad:
         with pytest.raises(ValueError):
             ra.kv_store_rope(pool, r, **{**good, **kw})
-    assert ra._rows("q", wide[:, :32], 4, 32, 128, BF) == 48 * 128      # a slice of one projection's output
+    # host tensors in a good layout (here slices of one projection's output) are refused for where they are
+    with pytest.raises((ValueError, RuntimeError)):
+        ra.kv_store_rope(pool, r, slots, slots, wide[:, 32:40], wide[:, 40:], wide[:, :32], torch.zeros_like(q))
     with pytest.raises(ValueError):
         ra.make_rope_desc(torch.zeros(4, 128, dtype=BF))
     with pytest.raises(ValueError):
