@@ -342,20 +342,29 @@ def plan_from_rows(rows: list) -> dict:
 class DeviceEngine:
     """KV pool + slot tables in HBM and the kernel launches of one batch."""
 
-    def __init__(self, shape, pool_slots: int, device="cuda", kv_fp8: bool = False):
+    def __init__(self, shape, pool_slots: int, device="cuda", kv_fp8: bool = False, kv_fp4: bool = False):
         import torch
         self.torch = torch
         self._lib = lib()    # raises if the library is missing
         self.shape = shape
         self.device = torch.device(device)
-        self.kv_fp8 = bool(kv_fp8)
+        self.kv_fp8, self.kv_fp4 = bool(kv_fp8), bool(kv_fp4)
+        if kv_fp8 and kv_fp4:
+            raise ValueError("a pool is held in one format: kv_fp8 or kv_fp4")
         dev = self.device
-        self.k_scale = self.v_scale = None
+        self.k_scale = self.v_scale = self.k_bscale = self.v_bscale = None
         if shape.mla:
             if kv_fp8:
                 raise ValueError("FP8 pools are GQA only")
+            if kv_fp4:
+                raise ValueError("4-bit pools are GQA only")
             self.pool_k = torch.zeros(pool_slots, shape.head_dim_k, dtype=torch.bfloat16, device=dev)
             self.pool_v = None
+        elif kv_fp4:  # E2M1 codes, two per byte, and a scale byte per 16 of them
+            codes = lambda d: torch.zeros(pool_slots, shape.kv_heads, d // 2, dtype=torch.uint8, device=dev)
+            scales = lambda d: torch.zeros(pool_slots, shape.kv_heads, d // 16, dtype=torch.uint8, device=dev)
+            self.pool_k, self.pool_v = codes(shape.head_dim_k), codes(shape.head_dim_v)
+            self.k_bscale, self.v_bscale = scales(shape.head_dim_k), scales(shape.head_dim_v)
         elif kv_fp8:  # E4M3 codes and one fp32 scale per (slot, KV head) row
             self.pool_k = torch.zeros(pool_slots, shape.kv_heads, shape.head_dim_k, dtype=torch.uint8, device=dev)
             self.pool_v = torch.zeros(pool_slots, shape.kv_heads, shape.head_dim_v, dtype=torch.uint8, device=dev)
@@ -366,7 +375,8 @@ class DeviceEngine:
             self.pool_v = torch.zeros(pool_slots, shape.kv_heads, shape.head_dim_v, dtype=torch.bfloat16, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.pool = make_pool_desc(self.pool_k, self.pool_v, self.err, mla=shape.mla, head_dim_v=shape.head_dim_v,
-                                   k_scale=self.k_scale, v_scale=self.v_scale)
+                                   k_scale=self.k_scale, v_scale=self.v_scale, k_bscale=self.k_bscale,
+                                   v_bscale=self.v_bscale)
         self.desc = make_attn_desc(self.pool, shape.q_heads, shape.scale)
         self.sms = torch.cuda.get_device_properties(dev).multi_processor_count if dev.type == "cuda" else 1
         self._ws = torch.zeros(1 << 20, dtype=torch.uint8, device=dev)
@@ -377,7 +387,8 @@ class DeviceEngine:
         self.pack_wait_s = 0.0       # pack() time blocked on the GPU (on whichever thread packs)
         self.timing = False          # record CUDA events around device calls
         self.timing_every = 1        # decode steps: events on every n-th step only
-        self.fuse_store = not kv_fp8  # decode steps store the new token inside attn_decode_append (bf16 pools)
+        # decode steps store the new token inside attn_decode_append (bf16 pools)
+        self.fuse_store = not (kv_fp8 or kv_fp4)
         self.events = {}             # call name -> [(start, end, info)]
         self.launches = 0            # kernels launched by the library (counted per call)
         self.host_wait_s = 0.0       # host time blocked on the GPU (staging buffer reuse)

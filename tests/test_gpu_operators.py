@@ -683,3 +683,39 @@ def test_two_streams_with_their_own_workspaces(cuda):
     assert ra.rc_sync(pool.err) == ra.RC_OK
     for x in both:
         assert torch.equal(x[0], alone[0]) and torch.equal(x[1], alone[1])
+
+
+@pytest.mark.parametrize("cascade", [True, False])
+def test_few_shot_workload_over_a_4_bit_pool(cuda, cascade):
+    """The few-shot workload (reduced) through the scheduler and the engine: prefill over the cached examples, decode
+    steps storing each new token; sampled requests against the oracle on the oracle's own quantisation."""
+    from radixattention_prefix_shared_tree_gb300 import workloads as wl
+    from radixattention_prefix_shared_tree_gb300.driver import DeviceEngine
+    from synth import traces
+    from synth.model import SynthModel
+    tr = traces.few_shot(n_questions=40, max_new=5)
+    sh = tr.shape
+    model = SynthModel(sh, tr.seed, tr.vocab, device=cuda)
+    eng = DeviceEngine(sh, 1 << 16, device=cuda, kv_fp4=True)
+    runner = wl.Runner(ra.RadixCache(1 << 16), model, eng, policy=ra.RC_LPM, cascade=cascade, collect=True)
+    reqs = wl.run_few_shot(runner, tr)
+    assert ra.rc_sync(eng.err) == ra.RC_OK
+    assert runner.last_layout.use_cascade == cascade
+    for r in reqs[::6]:
+        h = model.hashes(r.rid)
+        pos, out, lse = runner.extend_out[r.rid]
+        pos, out, lse = list(pos), [out], [lse]
+        for p, o, l in runner.decode_out[r.rid]:
+            pos.append(p)
+            out.append(o[None])
+            lse.append(l[None])
+        n = max(pos) + 1
+        held = [f4.dequantize(*f4.quantize(hg.bf16_bits_to_f32(hg.gen_values(h[:n], kind, sh.kv_heads, sh.head_dim_k)
+                                                               .reshape(n, sh.kv_heads, -1))))
+                for kind in (hg.KIND_K, hg.KIND_V)]
+        q = hg.bf16_bits_to_f32(hg.gen_values(h[np.asarray(pos)], hg.KIND_Q, sh.q_heads, sh.head_dim_k)
+                                .reshape(len(pos), sh.q_heads, -1)).astype(np.float64)
+        ref, rl, a = f4.attention(q, *held, [np.arange(p + 1) for p in pos], sh.q_heads, sh.kv_heads, sh.scale)
+        got = hg.bf16_bits_to_f32(np.concatenate([np.asarray(o).reshape(-1, sh.q_heads, sh.head_dim_v) for o in out]))
+        tol.check_values(got, ref, a, u_p=tol.U_F16, label="fp4 workload")
+        tol.check_lse(np.concatenate([np.asarray(l).reshape(-1, sh.q_heads) for l in lse]), rl)
