@@ -537,7 +537,9 @@ rc_status attn_decode_static(const rc_attn_desc* desc, const void* q, const rc_k
                              int32_t batch, const rc_cascade* cascade, void* out, float* lse,
                              rc_stream_t stream);
 
-/* Workspace bytes attn_extend needs (0 today; kept for split variants). */
+/* Workspace bytes with which attn_extend splits long rows of a small batch over
+ * more CTAs (4-bit pools; 0 for the others, and where splitting gains nothing).
+ * Without that workspace it computes the same rows unsplit. */
 rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
                                 int32_t max_len, size_t* bytes);
 
@@ -547,6 +549,8 @@ rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
  * stored).  New token i of row b (position p = len[b]-n_b+i) attends to keys
  * 0..p causally.  q and out: [sum n_b][q_heads][head_dim] bf16.
  * max_q: host bound on n_b.  lse: NULL or [sum n_b][q_heads] fp32.
+ * ws: NULL, or attn_extend_workspace bytes, 256-byte aligned; calls that can
+ * overlap on the GPU need a workspace each.
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED, RC_ERR_CUDA. */
 rc_status attn_extend(const rc_attn_desc* desc, const void* q, const int32_t* qo_indptr,
                       const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out,

@@ -11,10 +11,12 @@
 //  * more: the tcgen05 kernel of attn_extend without the causal edge, 256
 //    pairs per CTA, bound by its softmax and matrix work; where its grid would
 //    leave SMs idle the keys are split over CTAs.
-// Split keys leave normalised partials that cross_merge_kernel joins.
+// Split keys leave normalised partials that a merge joins (attn_split_merge.cuh,
+// or for the 4-bit table pass merge_runs_kernel).
 
 #include "attn_decode_fp4.cuh"
 #include "attn_decode_split.cuh"
+#include "attn_split_merge.cuh"
 #include "attn_tc2.cuh"
 
 namespace {
@@ -40,19 +42,20 @@ rc_status plan_cross(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_
     const int64_t cols = (int64_t)max_q * G;
     pl->few = cols <= kFewColumns;
     int64_t splits = 1, step;
-    if (pl->few) {  // as attn_decode: one wave of warps, at least 64 keys each
+    int64_t unit = kDecKeys;         // chunks are multiples of this many keys
+    if (pl->few) {  // one wave of warps, at least two 16-key tiles each
         const int64_t base = (int64_t)batch * hkv;
         if (base > 0 && base < 8 * sms) splits = kWarpsPerCta * sms / base;
-        step = kDecKeys;
-    } else {  // one CTA per SM, at least 256 keys each
+        step = unit = 2 * kWarpKeys;
+    } else {  // one CTA per SM, at least two 64-key tiles each
         const int64_t grid = ((cols + rc_tc2::ROWS - 1) / rc_tc2::ROWS) * hkv * batch;
         if (grid > 0 && grid < sms) splits = sms / grid;
-        step = 256;
+        step = 2 * rc_tc2::TN;
     }
     const int64_t most = max_len > 0 ? (max_len + step - 1) / step : 1;
     splits = splits < 1 ? 1 : splits > most ? most : splits;
     int64_t chunk = max_len > 0 ? (max_len + splits - 1) / splits : kDecKeys;
-    chunk = (chunk + kDecKeys - 1) / kDecKeys * kDecKeys;
+    chunk = (chunk + unit - 1) / unit * unit;
     if (chunk > 0x7fffffc0) return RC_ERR_ARG;
     pl->chunk = (int)chunk;
     pl->n_chunks = max_len > 0 ? (int)((max_len + chunk - 1) / chunk) : 1;
@@ -90,53 +93,6 @@ rc_status check_pool(const rc_attn_desc* d) {
     }
     if (fmt == rc::kFmtFp4) return rc_host::check_fp4(P);
     return RC_OK;
-}
-
-// One warp per (token, head): joins the row's n_chunks partials.  The block's
-// token is token i of row b; a row that the pass refused has none.
-template <int D>
-__global__ void __launch_bounds__(256) cross_merge_kernel(const float* __restrict__ part_o,
-                                                          const float* __restrict__ part_lse, int n_chunks,
-                                                          const int32_t* __restrict__ qo_indptr, int max_q,
-                                                          int64_t max_rows, int q_heads,
-                                                          __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                                                          const int32_t* err) {
-    constexpr int PER = D / 32;
-    grid_dep_wait();
-    const int b = blockIdx.x / max_q, i = blockIdx.x % max_q;
-    const int qo0 = qo_indptr[b], nq = qo_indptr[b + 1] - qo0;
-    if (nq > max_q || qo0 < 0 || (int64_t)qo0 + nq > max_rows || i >= nq) return;
-    // a pass that gave up on a bounded wait left partials unwritten
-    if (err && (*reinterpret_cast<const volatile int32_t*>(err) & rc::kErrTimeout)) return;
-    const int lane = threadIdx.x & 31;
-    for (int h = threadIdx.x >> 5; h < q_heads; h += 8) {
-        const int64_t row = (int64_t)(qo0 + i) * q_heads + h;
-        const float* pl = part_lse + row * n_chunks;
-        const float* po = part_o + row * n_chunks * D + lane;
-        float m = -INFINITY;
-        for (int c = lane; c < n_chunks; c += 32) m = fmaxf(m, pl[c]);
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-        float w = 0.f, acc[PER];
-#pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-        if (m != -INFINITY) {
-#pragma unroll 4
-            for (int c = 0; c < n_chunks; ++c) {
-                const float l2 = pl[c];
-                const float wc = l2 == -INFINITY ? 0.f : rc::fast_exp2(l2 - m);
-                w += wc;
-                if (wc != 0.f) {
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) acc[k] += wc * po[(int64_t)c * D + 32 * k];
-                }
-            }
-        }
-        const float inv = w > 0.f ? 1.f / w : 0.f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) out[row * D + lane + 32 * k] = __float2bfloat16_rn(acc[k] * inv);
-        if (lse && lane == 0) lse[row] = w > 0.f ? (m + log2f(w)) * rc::kLn2 : -INFINITY;
-    }
 }
 
 template <auto Kernel, int WARPS, bool RUNS = false>
@@ -279,18 +235,8 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     if (pl.runs)
         return rc_host::launch_status(wide ? launch_merge_runs<128, true>(dp, max_rows, st)
                                            : launch_merge_runs<64, true>(dp, max_rows, st));
-    // the merge starts as the pass's CTAs leave and waits for its end inside
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)max_rows);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, wide ? cross_merge_kernel<128> : cross_merge_kernel<64>, (const float*)part_o,
-                           (const float*)part_lse, pl.n_chunks, qo_indptr, max_q, max_rows, desc->q_heads,
-                           static_cast<__nv_bfloat16*>(out), lse, (const int32_t*)P.err);
+    const rc_dec::SplitMerge m{part_o, part_lse, pl.n_chunks, qo_indptr, max_q, max_rows, desc->q_heads,
+                               static_cast<__nv_bfloat16*>(out), lse, P.err};
+    e = wide ? launch_split_merge<128>(m, st) : launch_split_merge<64>(m, st);
     return rc_host::launch_status(e);
 }

@@ -69,10 +69,12 @@ RC_DEV int64_t runs_of(int64_t tiles, int most) {
     const int64_t r = (tiles + kMinTiles - 1) / kMinTiles;
     return r < most ? r : most;
 }
-// One warp per (row, KV head) and no merge: rows short enough, and enough of
-// them, that a warp each fills most of the SMs.
+// One warp per (row, KV head) and no merge: rows of three tiles at most (their
+// merge would take longer: 4 rows of 96 keys 9.8 us in runs), or short ones
+// and enough of them that a warp each fills most of the SMs.
 inline bool whole_rows(int64_t batch, int64_t kv_heads, int64_t max_len, int64_t sms) {
-    return 2 * batch * kv_heads >= (int64_t)kWarps * kCtasPerSm * sms && max_len <= 512;
+    return max_len <= 3 * kKeys ||
+           (2 * batch * kv_heads >= (int64_t)kWarps * kCtasPerSm * sms && max_len <= 512);
 }
 
 // Shared-memory row of V's key m (0..31): inside each 16 keys the even ones

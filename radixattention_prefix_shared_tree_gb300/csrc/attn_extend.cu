@@ -12,6 +12,7 @@
 // MMA and softmax warps; bf16 output written directly (no split, no
 // workspace).
 
+#include "attn_split_merge.cuh"
 #include "attn_tc2.cuh"
 #include "common.cuh"
 
@@ -23,7 +24,7 @@ cudaError_t launch_extend(const rc::MQParams& p, int batch, int max_q, int kv_he
     cudaError_t e = rc_host::ensure_smem<rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT>>(smem);
     if (e != cudaSuccess) return e;
     constexpr int TPC = rc_tc2::ROWS / G;
-    dim3 grid((max_q + TPC - 1) / TPC, kv_heads, batch);
+    dim3 grid((max_q + TPC - 1) / TPC, kv_heads, batch * p.seg_chunks);
     rc_tc2::attn_tc2_kernel<D, G, rc::MQMode::kExtend, FMT><<<grid, rc_tc2::threads<FMT>(), smem, st>>>(p);
     return cudaGetLastError();
 }
@@ -40,20 +41,51 @@ cudaError_t dispatch(int G, const rc::MQParams& p, int batch, int max_q, int kv_
     }
 }
 
+// Over a 4-bit pool, a grid that would leave most SMs idle splits the keys, at
+// least four tiles a CTA, where there are enough of them to pay for the
+// merge (1 row of 8 tokens over 4,000 keys: 57 us whole, 12 split; 4 rows of 40
+// over 340: 12.3 whole, 14.1 split; over 1,040: 22.4 and 16.3).
+constexpr int kSplitKeys = 512;
+struct ExtendPlan {
+    int chunk = 0, n_chunks = 1;
+    size_t part_o = 0, total = 0;
+};
+
+ExtendPlan plan_extend(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_t max_len) {
+    ExtendPlan pl;
+    const rc_pool_desc& P = d->pool;
+    if (rc_host::pool_format(P) != rc::kFmtFp4 || P.kv_heads <= 0 || max_len < kSplitKeys || batch <= 0 ||
+        max_q <= 0)
+        return pl;
+    const int64_t G = d->q_heads / P.kv_heads;
+    const int64_t grid = ((max_q * G + rc_tc2::ROWS - 1) / rc_tc2::ROWS) * P.kv_heads * batch;
+    const int64_t most = (max_len + 4 * rc_tc2::TN - 1) / (4 * rc_tc2::TN);
+    int64_t splits = rc_host::sm_count() / (grid > 0 ? grid : 1);
+    splits = splits < most ? splits : most;
+    const int64_t max_rows = (int64_t)batch * max_q;
+    if (splits < 2 || batch * splits > 65535 || max_rows > 0x7fffffff) return pl;
+    const int64_t chunk = (max_len + splits - 1) / splits;
+    pl.chunk = (int)((chunk + rc_tc2::TN - 1) / rc_tc2::TN * rc_tc2::TN);
+    pl.n_chunks = (max_len + pl.chunk - 1) / pl.chunk;
+    if (pl.n_chunks < 2) return ExtendPlan();
+    const size_t rows = (size_t)max_rows * d->q_heads * pl.n_chunks;
+    pl.part_o = (rows * P.head_dim_v * sizeof(float) + 255) & ~size_t(255);
+    pl.total = pl.part_o + ((rows * sizeof(float) + 255) & ~size_t(255));
+    return pl;
+}
+
 }  // namespace
 
 extern "C" rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
                                            int32_t max_len, size_t* bytes) {
     if (!desc || !bytes || batch < 0 || max_q < 0 || max_len < 0) return RC_ERR_ARG;
-    *bytes = 0;
+    *bytes = plan_extend(desc, batch, max_q, max_len).total;
     return RC_OK;
 }
 
 extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const int32_t* qo_indptr,
                                  const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out, float* lse,
                                  void* ws, size_t ws_bytes, rc_stream_t stream) {
-    (void)ws;
-    (void)ws_bytes;
     if (!desc || !kv || batch < 0 || max_q < 0) return RC_ERR_ARG;
     if (batch == 0 || max_q == 0) return RC_OK;
     if (!q || !qo_indptr || !out || !kv->slots || !kv->start || !kv->len || !desc->pool.k) return RC_ERR_ARG;
@@ -90,6 +122,18 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
     p.v_scale = fp8 ? P.v_scale : nullptr;
     p.k_bscale = fmt == rc::kFmtFp4 ? P.k_bscale : nullptr;
     p.v_bscale = fmt == rc::kFmtFp4 ? P.v_bscale : nullptr;
+    // without a workspace, or with one too small, every row's keys stay with one CTA
+    ExtendPlan pl = plan_extend(desc, batch, max_q, kv->max_len);
+    if (pl.n_chunks > 1 && (!ws || ws_bytes < pl.total)) pl = ExtendPlan();
+    if (pl.n_chunks > 1 && (reinterpret_cast<uintptr_t>(ws) & 255)) return RC_ERR_ARG;
+    const int64_t max_rows = (int64_t)batch * max_q;
+    p.seg_chunk = pl.chunk;
+    p.seg_chunks = pl.n_chunks;
+    p.max_q = max_q;
+    p.max_len = kv->max_len;
+    p.max_rows = max_rows;
+    p.part_o = static_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.part_o);
     const int G = desc->q_heads / P.kv_heads;
     bool ok = false;
     cudaError_t e = cudaSuccess;
@@ -105,5 +149,9 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
         e = dispatch<64, rc::kFmtBf16>(G, p, batch, max_q, P.kv_heads, st, &ok);
     }
     if (!ok) return RC_ERR_UNSUPPORTED;
-    return rc_host::launch_status(e);
+    if (e != cudaSuccess || pl.n_chunks == 1) return rc_host::launch_status(e);
+    const rc_dec::SplitMerge m{p.part_o, p.part_lse, pl.n_chunks, qo_indptr, max_q, max_rows, desc->q_heads, p.out, lse,
+                               P.err};
+    return rc_host::launch_status(P.head_dim_k == 128 ? rc_dec::launch_split_merge<128>(m, st)
+                                                      : rc_dec::launch_split_merge<64>(m, st));
 }

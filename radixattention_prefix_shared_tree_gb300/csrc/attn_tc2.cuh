@@ -309,18 +309,39 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     int n_rows_tok, key_count, prefix = 0, qo0, chunk = 0;
     const int32_t* keys;
     if constexpr (MODE == rc::MQMode::kExtend) {
-        qo0 = p.qo_indptr[z];
-        n_rows_tok = p.qo_indptr[z + 1] - qo0;
-        const int L = p.len[z];
+        const int b = z / p.seg_chunks;
+        chunk = z % p.seg_chunks;
+        qo0 = p.qo_indptr[b];
+        n_rows_tok = p.qo_indptr[b + 1] - qo0;
+        const int L = p.len[b];
         prefix = L - n_rows_tok;
-        const int64_t row0 = p.start[z];
-        if (tok0 >= n_rows_tok) return;
-        if (row0 < 0 || prefix < 0 || row0 + L > p.table_len) {
-            if (tid == 0) rc::flag_error(p.err, rc::kErrBadSlot);
+        const int64_t row0 = p.start[b];
+        if (p.seg_chunks > 1 && (n_rows_tok > p.max_q || qo0 < 0 || (int64_t)qo0 + n_rows_tok > p.max_rows)) {
+            if (tid == 0) rc::flag_error(p.err, rc::kErrBadSlot);  // more tokens than the partials have room for
             return;
         }
-        keys = p.table + row0;
+        if (tok0 >= n_rows_tok) return;
+        if (row0 < 0 || prefix < 0 || row0 + L > p.table_len || (p.seg_chunks > 1 && L > p.max_len)) {
+            if (tid == 0) rc::flag_error(p.err, rc::kErrBadSlot);
+            if (p.seg_chunks > 1)  // (the merge reads what is written here)
+                for (int i = tid; i < min(n_rows_tok - tok0, TPC) * G; i += THREADS)
+                    p.part_lse[((int64_t)(qo0 + tok0 + i / G) * p.q_heads + kvh * G + i % G) * p.seg_chunks + chunk] =
+                        -INFINITY;
+            return;
+        }
+        const int k0 = chunk * p.seg_chunk;
+        prefix -= k0;  // the first token's position, counted from the chunk's first key
+        keys = p.table + row0 + k0;
         key_count = prefix + min(n_rows_tok, tok0 + TPC);
+        if (p.seg_chunks > 1) {
+            key_count = min(key_count, p.seg_chunk);
+            if (key_count <= 0) {  // none of these tokens sees a key of the chunk
+                for (int i = tid; i < min(n_rows_tok - tok0, TPC) * G; i += THREADS)
+                    p.part_lse[((int64_t)(qo0 + tok0 + i / G) * p.q_heads + kvh * G + i % G) * p.seg_chunks + chunk] =
+                        -INFINITY;
+                return;
+            }
+        }
     } else if constexpr (MODE == rc::MQMode::kCross) {
         const int b = z / p.seg_chunks;
         chunk = z % p.seg_chunks;
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         if (q < n_qt) {
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             const float lse2 = l_run > 0.f ? m_used + log2f(l_run) : -INFINITY;
-            const bool whole = MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1);
+            const bool whole = MODE != rc::MQMode::kCascade && p.seg_chunks == 1;
             unsigned char* stg = sQ + warp * 32 * D * 2;
             // n 16-byte chunks of every row of the warp, staged, to row `rw` of dst
             // (its rows `stride` 16-byte units apart)
@@ -733,7 +754,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             }
             if (ok && row_valid) {
                 const int h = kvh * G + (row % G);
-                if (MODE == rc::MQMode::kExtend || (MODE == rc::MQMode::kCross && p.seg_chunks == 1)) {
+                if (whole) {
                     if (p.lse) p.lse[(int64_t)(qo0 + r_tok) * p.q_heads + h] = lse2 * rc::kLn2;
                 } else {
                     p.part_lse[((int64_t)(qo0 + r_tok) * p.q_heads + h) * p.seg_chunks + chunk] = lse2;

@@ -51,8 +51,9 @@ struct MQParams {
     // 4-bit pool: pool_k / pool_v hold E2M1 codes and these the block scales
     const uint8_t* k_bscale;  // [n_slots][kv_heads][D / 16]
     const uint8_t* v_bscale;
-    // cross: the caller's bounds on a row's tokens, all tokens and a row's keys
-    // (seg_chunk keys a CTA, seg_chunks CTAs a row: grid z = row * seg_chunks + chunk)
+    // cross, extend: the caller's bounds on a row's tokens, all tokens and
+    // (cross) a row's keys; seg_chunk keys a CTA, seg_chunks CTAs a row: grid
+    // z = row * seg_chunks + chunk; with more than one, partials as the cascade's
     int32_t max_q;
     int32_t max_len;
     int64_t max_rows;

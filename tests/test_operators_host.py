@@ -165,7 +165,7 @@ def test_attn_cross_refusals(built):
 def test_attn_cross_workspace(built):
     desc = ra.make_attn_desc(bf16_pool(), 32, 0.1)
     assert ra.attn_cross_workspace(desc, 64, 1024, 4096) == 0          # the grid fills the SMs
-    assert ra.attn_cross_workspace(desc, 1, 1, 64) == 0                # nothing to split
+    assert ra.attn_cross_workspace(desc, 1, 1, 32) == 0                # nothing to split
     assert ra.attn_cross_workspace(desc, 0, 4, 64) == 0 and ra.attn_cross_workspace(desc, 4, 0, 64) == 0
     small = ra.attn_cross_workspace(desc, 1, 1, 4096)
     assert small >= 2 * 32 * 129 * 4
