@@ -302,7 +302,8 @@ rc_status bc_stats(bc_cache* cache, rc_stats_t* out);
  * block: [n_slots][kv_heads][head_dim/16], an unsigned float of 5 exponent
  * bits (bias 15) and 3 mantissa bits, i.e. bits 14..7 of an f16.  An element's
  * value is its code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times its
- * block's scale, always an f16 value.  Scale byte 0xff is a NaN: its block's
+ * block's scale, always an f16 value (so the queries of such a pool are taken
+ * as f16 too: exact below 65504 in magnitude).  Scale byte 0xff is a NaN: its block's
  * elements are NaN.  The four arrays are 16-byte aligned.  k_bscale and
  * v_bscale are read for such a pool only. */
 #define RC_KV_FP4 4
@@ -442,7 +443,8 @@ rc_status attn_decode_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
                                 const rc_cascade* cascade, size_t* bytes);
 
 /* One decode step for `batch` requests [LMI decode phase; N49 s.2]: row b's
- * single query q[b] ([batch][q_heads][head_dim_k] bf16) sits at the last
+ * single query q[b] ([batch][q_heads][head_dim_k] bf16; 4-bit pool: q and out
+ * 16-byte aligned) sits at the last
  * position of its context and attends to all of it:
  *   out[b][h] = sum_j softmax_j(sm_scale * q[b][h].K[j][g(h)]) V[j][g(h)]
  * over the cascade segments of row b (if any) and then its table row.
@@ -569,7 +571,7 @@ rc_status attn_cross_workspace(const rc_attn_desc* desc, int32_t batch, int32_t 
  * -infinity.  q and out: [sum n_b][q_heads][head_dim] bf16, 16-byte aligned;
  * rows of out behind the last token are not written.  lse: NULL or
  * [sum n_b][q_heads] fp32, natural log.  bf16, FP8 (head_dim 128) and 4-bit
- * pools, head_dim 64 or 128, 1, 2, 4 or 8 query heads per KV head.
+ * pools, head_dim 64 or 128, 1, 2, 4 or 8 query heads per KV head; sm_scale > 0.
  * ws: attn_cross_workspace bytes, 256-byte aligned (NULL when that is 0); calls
  * that can overlap on the GPU need a workspace each.
  * A row whose tokens exceed max_q, or reach beyond batch * max_q in all, is not

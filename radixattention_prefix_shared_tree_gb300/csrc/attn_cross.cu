@@ -165,6 +165,7 @@ extern "C" rc_status attn_cross(const rc_attn_desc* desc, const void* q, const i
     if (!desc || !kv || batch < 0 || max_q < 0 || kv->max_len < 0) return RC_ERR_ARG;
     rc_status s = check_pool(desc);
     if (s != RC_OK) return s;
+    if (!(desc->sm_scale > 0.f)) return RC_ERR_ARG;  // the largest score has to be the largest scaled one
     if (batch == 0 || max_q == 0) return RC_OK;
     if (!q || !qo_indptr || !out || !kv->slots || !kv->start || !kv->len) return RC_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;

@@ -368,7 +368,7 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
         if (k_new) return RC_ERR_UNSUPPORTED;
         s = rc_host::check_fp4(P);
         if (s != RC_OK) return s;
-        if (reinterpret_cast<uintptr_t>(q) & 15) return RC_ERR_ARG;
+        if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;
     }
     const int G = desc->q_heads / P.kv_heads;
     unsigned char* w = static_cast<unsigned char*>(ws);

@@ -573,6 +573,47 @@ def test_cross_one_row_per_key_equals_decode(cuda):
         check(b, None, ref, pool.u_p, label="cross")
 
 
+def test_pool_offsets_beyond_32_bits(cuda):
+    """Slots whose byte offsets pass 2^32 in a pool of nine million: stored with rotation, read by every call."""
+    n_slots, hq, hkv, d = 9_000_000, 16, 8, 128
+    assert n_slots * hkv * d // 2 > 1 << 32
+    err = torch.zeros(1, dtype=torch.int32, device=cuda)
+    k, v = (torch.zeros(n_slots, hkv, d // 2, dtype=torch.uint8, device=cuda) for _ in range(2))
+    ks, vs = (torch.zeros(n_slots, hkv, d // 16, dtype=torch.uint8, device=cuda) for _ in range(2))
+    pool = ra.make_pool_desc(k, v, err, k_bscale=ks, v_bscale=vs)
+    g = torch.Generator().manual_seed(3)
+    n = 300
+    slots = (n_slots - 1 - torch.randperm(500_000, generator=g)[:n]).to(torch.int32).to(cuda)
+    pos = torch.arange(n, dtype=torch.int32, device=cuda)
+    kn, vn, q = rand(g, n, hkv, d), rand(g, n, hkv, d), rand(g, n, hq, d)
+    cs = ra.rope_table(n, d, device=cuda)
+    qr = torch.empty_like(q)
+    ra.kv_store_rope(pool, ra.make_rope_desc(cs), slots, pos, kn, vn, q, qr)
+    t, p = cs.cpu().numpy(), pos.cpu().numpy()
+    kd = f4.dequantize(*f4.quantize(f4.rotate(f32(kn), t, p, 0, False)))
+    vd = f4.dequantize(*f4.quantize(f32(vn)))
+    desc = ra.make_attn_desc(pool, hq, 0.09)
+    one = lambda *a: torch.tensor(a, dtype=torch.int32, device=cuda)
+    kv = ra.make_kv_table(slots, one(0), one(n), n)
+    size = max(ra.attn_decode_workspace(desc, 1, n), ra.attn_cross_workspace(desc, 1, 40, n), 256)
+    ws = torch.empty(size, dtype=torch.uint8, device=cuda)
+    rows = [np.arange(n)] * n
+    qx = f32(qr).astype(np.float64)
+    ref = f4.attention(qx, kd, vd, rows, hq, hkv, float(np.float32(0.09)), p + 1)
+    full = f4.attention(qx[-40:], kd, vd, rows[:40], hq, hkv, float(np.float32(0.09)))
+    out = torch.empty_like(q)
+    ra.attn_extend(desc, qr, one(0, n), kv, 1, n, out)
+    check(out, None, ref, tol.U_F16, label="extend")
+    ra.attn_decode(desc, qr[-1:], kv, 1, out[-1:], None, ws)
+    check(out[-1:], None, [x[-1:] for x in ref], tol.U_F16, label="decode")
+    ra.attn_cross(desc, qr[-40:], one(0, 40), kv, 1, 40, out[-40:], None, ws)
+    check(out[-40:], None, full, tol.U_F16, label="cross")
+    ra.attn_cross(desc, qr[-1:], one(0, 1), kv, 1, 1, out[-1:], None, ws)
+    check(out[-1:], None, [x[-1:] for x in full], tol.U_F16, label="cross of one")
+    assert ra.rc_sync(err) == ra.RC_OK
+    assert int(k[:1000].max()) == 0
+
+
 # ---------------------------------------------------------------- together
 def _serve(cuda, fmt, graph):
     """Prefill and decode steps of a small batch with positions, then cross attention over an encoder's states, all

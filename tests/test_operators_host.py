@@ -127,10 +127,10 @@ def test_kv_store_rope_binding_checks_shapes(built):
         ra.make_rope_desc(torch.zeros(4, 256)[:, ::2])
 
 
-def call_cross(pool, hq=32, batch=2, max_q=16, max_len=64, ws=None, ws_bytes=0, **over):
+def call_cross(pool, hq=32, batch=2, max_q=16, max_len=64, ws=None, ws_bytes=0, scale=0.1, **over):
     buf = torch.zeros(1 << 14, dtype=BF)
     base = (buf.data_ptr() + 255) // 256 * 256
-    desc = ra.make_attn_desc(pool, hq, 0.1) if pool is not None else None
+    desc = ra.make_attn_desc(pool, hq, scale) if pool is not None else None
     a = dict(q=base, qo=base, out=base, slots=base, start=base, len=base)
     a.update(over)
     kv = ra.rc_kv_table(slots=a["slots"], start=a["start"], len=a["len"], max_len=max_len, table_len=128)
@@ -143,6 +143,8 @@ def test_attn_cross_refusals(built):
     assert call_cross(None) == A
     assert call_cross(bf16_pool(), batch=-1) == A and call_cross(bf16_pool(), max_q=-1) == A
     assert call_cross(bf16_pool(), max_len=-1) == A
+    for scale in (0.0, -0.1, float("nan")):
+        assert call_cross(bf16_pool(), scale=scale) == A
     assert call_cross(bf16_pool(), batch=0) == ra.RC_OK and call_cross(bf16_pool(), max_q=0) == ra.RC_OK
     for missing in ("q", "qo", "out", "slots", "start", "len"):
         assert call_cross(bf16_pool(), **{missing: None}) == A, missing
@@ -181,12 +183,12 @@ def test_fp4_pool_refused_where_unsupported(built):
     buf = torch.zeros(1 << 14, dtype=BF)
     b = (buf.data_ptr() + 255) // 256 * 256
 
-    def decode(pool, k_new=None, q=b, hq=32):
+    def decode(pool, k_new=None, q=b, hq=32, out=None):
         d = ra.make_attn_desc(pool, hq, 0.1)
         kv = ra.rc_kv_table(slots=b, start=b, len=b, max_len=16, table_len=64)
         if k_new:
             return L.attn_decode_append(C.byref(d), q, k_new, k_new, C.byref(kv), 2, None, b, None, b, 1 << 24, None)
-        return L.attn_decode(C.byref(d), q, C.byref(kv), 2, None, b, None, b, 1 << 24, None)
+        return L.attn_decode(C.byref(d), q, C.byref(kv), 2, None, out or b, None, b, 1 << 24, None)
 
     def extend(pool, q=b, hq=32):
         d = ra.make_attn_desc(pool, hq, 0.1)
@@ -199,7 +201,11 @@ def test_fp4_pool_refused_where_unsupported(built):
     odd.v_bscale = odd.v_bscale + 8
     for call in (decode, extend, store):
         assert call(no_scale) == A and call(odd) == A and call(deep) == U, call
+    empty = fp4_pool()
+    empty.n_slots = 0
+    assert decode(empty) == A and extend(empty) == A and store(empty) == A
     assert decode(fp4_pool(), k_new=b) == U          # appended keys: kv_store, then attn_decode
     assert decode(fp4_pool(), q=b + 2) == A and extend(fp4_pool(), q=b + 2) == A
+    assert decode(fp4_pool(), out=b + 8) == A
     assert decode(fp4_pool(), hq=24) == U
     assert store(fp4_pool(), v=None) == A and store(fp4_pool(), k=b + 8) == A
