@@ -304,7 +304,8 @@ rc_status bc_stats(bc_cache* cache, rc_stats_t* out);
  * value is its code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times its
  * block's scale, always an f16 value (so the queries of such a pool are taken
  * as f16 too: exact below 65504 in magnitude).  Scale byte 0xff is a NaN: its block's
- * elements are NaN.  The four arrays are 16-byte aligned.  k_bscale and
+ * elements are NaN, and a query row that reads them in K is NaN with lse
+ * +infinity.  The four arrays are 16-byte aligned.  k_bscale and
  * v_bscale are read for such a pool only. */
 #define RC_KV_FP4 4
 typedef struct rc_pool_desc {
@@ -551,6 +552,8 @@ rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
  * stored).  New token i of row b (position p = len[b]-n_b+i) attends to keys
  * 0..p causally.  q and out: [sum n_b][q_heads][head_dim] bf16.
  * max_q: host bound on n_b.  lse: NULL or [sum n_b][q_heads] fp32.
+ * An infinity or a NaN in a new token's V may make the row's earlier new tokens
+ * NaN too (a weight of zero times it).
  * ws: NULL, or attn_extend_workspace bytes, 256-byte aligned; calls that can
  * overlap on the GPU need a workspace each.
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED, RC_ERR_CUDA. */

@@ -249,8 +249,7 @@ RC_DEV void decode_epilogue(const DecParams& p, const Item& w, float* sE, float*
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
                 p.out[orow * D + lane + 32 * k] = __float2bfloat16_rn(acc[h][k] * inv);
-            if (p.lse && lane == 0)
-                p.lse[orow] = w_h[h] > 0.f ? (m_h[h] + log2f(w_h[h])) * rc::kLn2 : -INFINITY;
+            if (p.lse && lane == 0) p.lse[orow] = rc::log2_sum(m_h[h], w_h[h]) * rc::kLn2;
         }
     }
 }

@@ -459,12 +459,9 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         *reinterpret_cast<float2*>(sE + (2 * t_lane) * D + d0) = make_float2(o[mt][0] * inv0, o[mt][2] * inv0);
         *reinterpret_cast<float2*>(sE + (2 * t_lane + 1) * D + d0) = make_float2(o[mt][1] * inv1, o[mt][3] * inv1);
     }
-    // a NaN sum (a key whose block holds NaN) weighs as +infinity, so that the
-    // merge turns the row into NaN instead of skipping the partial
-    auto lse2 = [](float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; };
     if (g_lane == 0) {
-        sOwn[2 * t_lane] = lse2(m_run[0], l_run.x);
-        sOwn[2 * t_lane + 1] = lse2(m_run[1], l_run.y);
+        sOwn[2 * t_lane] = rc::log2_sum(m_run[0], l_run.x);
+        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1], l_run.y);
     }
     __syncwarp();
     if constexpr (FUSED) {
@@ -619,7 +616,7 @@ __global__ void __launch_bounds__(32 * fp4::kMergeWarps) merge_runs_kernel(const
                                                     rc::pack_bf16(acc[2] * inv, acc[3] * inv));
     else
         *out = rc::pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (p.lse && lane == 0) p.lse[orow] = wsum > 0.f ? (m + log2f(wsum)) * rc::kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[orow] = rc::log2_sum(m, wsum) * rc::kLn2;
 }
 
 // rows: batch rows, or (CROSS) their tokens; as the split pass's programmatic

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(32 * kSplitMergeWarps) split_merge_kernel(cons
     uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (V / 2);
 #pragma unroll
     for (int k = 0; k < V / 2; ++k) out[k] = rc::pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row] = wsum > 0.f ? (m + log2f(wsum)) * rc::kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = rc::log2_sum(m, wsum) * rc::kLn2;
 }
 
 // As the pass's programmatic dependent: its blocks start as that pass's leave

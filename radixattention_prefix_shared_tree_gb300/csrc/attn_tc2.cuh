@@ -5,17 +5,19 @@
 //
 // A CTA owns 256 query rows of one KV head -- two M=128 tiles, each (128/G
 // tokens or requests) x (the G query heads of that KV head) -- so every K/V
-// tile it gathers feeds both.  Eleven warps with fixed roles:
+// tile it gathers feeds both.  Eight softmax warps, NP producers (two for a
+// bf16 pool, three for codes) and one for the tensor core, with fixed roles:
 //   warps 0-3 and 4-7  softmax of query tile 0 and 1: one thread per row /
 //                      TMEM lane; read S from TMEM, write P (bf16) back over
 //                      it, rescale the row's O in TMEM when its max grows by
-//                      more than 2^8;
+//                      more than 2^8; at the end normalise O and write it out;
 //   warps 8..8+NP-1    producers, warp 8+i of the tiles t = i mod NP: gather
 //                      K/V rows by slot id with 16-byte cp.async into a
 //                      5-stage ring (no-swizzle operand layout), each lane's
 //                      copies arriving on the stage's mbarrier when they
-//                      land;
-//   warp 8+NP          issues every MMA (one thread) and owns TMEM.
+//                      land (their first tiles' before the set-up barrier);
+//   warp 8+NP          issues every MMA (one elected lane of the converged
+//                      warp) and owns TMEM.
 // Per 64-key tile and query tile q:  S_q = Q_q K^T (M=128, N=64, K=D) into
 // one of two S buffers, O_q += P_q V (M=128, N=D, K=64) with P read from
 // tensor memory.  The next tile's S products are issued before this tile's
@@ -25,7 +27,7 @@
 // (P over their first 32 columns), O at +128.  The tensor core runs one
 // thread's MMAs in issue order, so S(t+2) overwrites P(t) only after P(t).V
 // has read it.  All hand-offs are mbarriers; every wait is bounded and a wait
-// that gives up flags RC_ERR_TIMEOUT.  The MMA thread builds each
+// that gives up flags RC_ERR_TIMEOUT.  The MMA warp builds each
 // operand's descriptor once and steps it along K with 32-bit adds, and the
 // producers' copies of a row carry their offsets as immediates, so neither
 // spends issue slots on address arithmetic.
@@ -39,13 +41,15 @@
 // the V scales into P.  The ring has 4 stages (the scales take the room of
 // the fifth).
 //
-// 4-bit pool (E2M1 codes, one scale byte per 16 of them): as the FP8 pool, but
-// code times scale is itself an f16 value, so the producers store the pool's
-// exact values and the softmax is the bf16 pool's, with P in f16.
+// 4-bit pool (E2M1 codes, one scale byte per 16 of them): code times scale is
+// itself an f16 value, so the stages hold the pool's exact values and the
+// softmax is the bf16 pool's, with P in f16.  All three producers widen every
+// tile (Fp4Feed), from codes that cp.async brought two tiles ahead; 4 stages.
 //
 // Cross attention (kCross): extend without the causal edge, every token of
 // row z seeing all of the row's keys; with few rows of long keys the keys are
-// split over seg_chunks CTAs that leave partials, as the cascade does.
+// split over seg_chunks CTAs that leave partials, as the cascade does.  So does
+// extend over a 4-bit pool with few tokens.
 #pragma once
 
 #include "mq_attn.cuh"
@@ -75,7 +79,7 @@ __host__ __device__ constexpr int stages() {
     return FMT == rc::kFmtFp8 ? NS_FP8 : FMT == rc::kFmtFp4 ? NS_FP4 : NS_BF16;
 }
 template <int FMT>
-__host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FMT>() + 4 + 4 + 2; }
+__host__ __device__ constexpr int n_bars() { return 1 + 2 * stages<FMT>() + 4 + 4 + 2 + 1; }
 
 // 4-bit pool: every producer warp takes every NP-th group of eight keys of every
 // tile.  Its part of a tile as the pool holds it (K codes, V codes, K scales, V
@@ -219,6 +223,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     uint64_t* s_full = bar + 1 + 2 * NS;     // [QT][2], count 1
     uint64_t* p_full = s_full + 4;           // [QT][2] (one per S buffer), count 4 (the tile's softmax warps)
     uint64_t* o_done = p_full + 4;           // [QT], count 1
+    uint64_t* drained = o_done + QT;         // count 1: products in flight when a wait gave up
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -437,6 +442,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
             for (int q = 0; q < QT; ++q) {
                 tc::mbar_init(&o_done[q], 1);
             }
+            tc::mbar_init(drained, 1);
             tc::fence_mbar_init();
         }
         __syncwarp();
@@ -698,7 +704,9 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         // instruction would touch 32 rows, one tag each: 2.6 us a CTA.)
         if (q < n_qt) {
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            const float lse2 = l_run > 0.f ? m_used + log2f(l_run) : -INFINITY;
+            const float lse2 = FP4 || MODE == rc::MQMode::kCross ? rc::log2_sum(m_used, l_run)
+                               : l_run > 0.f                     ? m_used + log2f(l_run)
+                                                                 : -INFINITY;
             const bool whole = MODE != rc::MQMode::kCascade && p.seg_chunks == 1;
             unsigned char* stg = sQ + warp * 32 * D * 2;
             // n 16-byte chunks of every row of the warp, staged, to row `rw` of dst
@@ -928,11 +936,19 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     tc::commit(&o_done[q]);
                 }
             }
-            if (lead) tc::commit(&kv_empty[st]);  // the stage is free once everything issued so far is done
+            // the stage is free once everything issued so far is done (a last use
+            // has nobody to tell, and the CTA must not leave an arrival behind)
+            if (lead && t + NS < nt) tc::commit(&kv_empty[st]);
             st = st1;
             ph = ph1;
         }
-        if (!ok && lead) rc::flag_error(p.err, rc::kErrTimeout);
+        if (!ok) {
+            if (lead) {
+                rc::flag_error(p.err, rc::kErrTimeout);
+                tc::commit(drained);
+            }
+            tc::mbar_wait(drained, 0, kWaitIter);  // the products read stages and write TMEM
+        }
         __syncwarp();
     }
     if constexpr (MODE == rc::MQMode::kCascade) {

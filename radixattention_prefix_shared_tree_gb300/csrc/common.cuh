@@ -216,6 +216,11 @@ RC_DEV uint32_t pack_bf16(float lo, float hi) {
 
 RC_DEV float fast_exp2(float x) { return exp2f(x); }
 
+// A softmax part's log-sum-exp in log2 units from its reference m and sum l.
+// None: -infinity, no weight.  A NaN sum (a key of the part is NaN): +infinity,
+// so that a merge turns the row into NaN instead of leaving the part out.
+RC_DEV float log2_sum(float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; }
+
 // Byte offset of 16-byte chunk `c` of row `r` in a tile whose rows are
 // `chunks` 16-byte chunks long, XOR-swizzled on the low three bits so that
 // ldmatrix over 8 consecutive rows touches 8 different bank groups.

@@ -369,6 +369,51 @@ def test_decode_fp4_nan_blocks_and_bad_slots(cuda):
     assert ra.rc_sync(pool.err) == ra.RC_ERR_DEVICE
 
 
+@pytest.mark.parametrize("call,fmt,nq", [("decode", "fp4", 1), ("extend", "fp4", 8), ("extend", "fp4", 300),
+                                         ("cross", "bf16", 1), ("cross", "fp8", 1), ("cross", "fp4", 1),
+                                         ("cross", "bf16", 40), ("cross", "fp8", 40), ("cross", "fp4", 40)])
+def test_nan_key_of_a_split_row(cuda, call, fmt, nq):
+    """A NaN key in one part of a row's keys: NaN for the heads that read it, lse +infinity, the rest as without it."""
+    hq, hkv, d = 8, 2, 128
+    pool = Pool(fmt, 4000, hkv, d, cuda, 11)
+    lens = [1500, 1400, 700]
+    rows, table, start, length = tables(lens, 4000, 5, cuda)
+    rows[1] = np.arange(100, 1500, dtype=np.int32)       # row 1's keys are no other row's
+    others = np.concatenate([np.arange(100), np.arange(1500, 4000)]).astype(np.int32)
+    rows[0], rows[2] = others[:1500], others[1500:2200]
+    table = torch.from_numpy(np.concatenate(rows)).to(cuda)
+    q = rand(torch.Generator().manual_seed(2), 3 * nq, hq, d)
+    qo = torch.arange(4, dtype=torch.int32, device=cuda) * nq
+    desc = ra.make_attn_desc(pool.desc, hq, 0.1)
+    kv = ra.make_kv_table(table, start, length, 1500)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=cuda)
+
+    def run():
+        out, lse = torch.zeros_like(q), torch.zeros(3 * nq, hq, dtype=torch.float32, device=cuda)
+        if call == "decode":
+            ra.attn_decode(desc, q, kv, 3, out, lse, ws)
+        elif call == "cross":
+            ra.attn_cross(desc, q, qo, kv, 3, nq, out, lse, ws)
+        else:
+            ra.attn_extend(desc, q, qo, kv, 3, nq, out, lse, ws)
+        assert ra.rc_sync(pool.err) == ra.RC_OK
+        return out, lse
+
+    clean, clean_lse = run()
+    slot = int(rows[1][300])
+    if fmt == "bf16":
+        pool.k[slot, 1, 5] = float("nan")
+    elif fmt == "fp8":
+        pool.ks[slot, 1] = float("nan")
+    else:
+        pool.ks[slot, 1, 3] = 255
+    out, lse = run()
+    hit = torch.zeros(3 * nq, hq, dtype=torch.bool, device=cuda)
+    hit[nq:2 * nq, 4:] = True
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isposinf(lse[hit]).all())
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (64, 8, 128), (4, 4, 64)])
 def test_cascade_fp4_vs_oracle(cuda, hq, hkv, d):
     """A shared segment read once for all rows, on both grids, equals the flat rows' oracle."""
