@@ -68,11 +68,11 @@ __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.w
 struct Item {
     int b, kvh, chunk, ncol, L, k0, count;
     int64_t row0;        // the row's first entry in the table
-    int64_t qrow0;       // flat (token, head) row of column 0
+    int64_t qrow0;       // CROSS: flat (token, head) row of column 0
     int q_heads, group;
     template <bool CROSS>
     RC_DEV int64_t qrow(int c) const {
-        return CROSS ? qrow0 + (int64_t)(c / group) * q_heads + c % group : qrow0 + c;
+        return CROSS ? qrow0 + (int64_t)(c / group) * q_heads + c % group : (int64_t)b * q_heads + kvh * group + c;
     }
 };
 
@@ -88,7 +88,7 @@ RC_DEV Item decode_item(const DecParams& p, int it, int lane) {
     w.row0 = p.start[w.b];
     w.L = p.len[w.b];
     w.q_heads = p.q_heads;
-    w.group = p.group;
+    w.group = CROSS ? p.group : NC;
     bool bad = w.row0 < 0 || w.L < 0 || w.row0 + w.L > p.table_len;
     if constexpr (CROSS) {
         const int qo0 = p.qo_indptr[w.b], nq = p.qo_indptr[w.b + 1] - qo0;
@@ -99,7 +99,7 @@ RC_DEV Item decode_item(const DecParams& p, int it, int lane) {
         bad = bad || w.L > p.max_len;
     } else {
         w.ncol = NC;
-        w.qrow0 = (int64_t)w.b * p.q_heads + w.kvh * NC;
+        w.qrow0 = 0;
     }
     if (bad) {  // row outside the table: read nothing
         if (lane == 0 && w.kvh == 0 && w.chunk == 0) rc::flag_error(p.err, rc::kErrBadSlot);

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     } else {
         w.kvh = it % p.kv_heads;
         w.q_heads = p.q_heads;
-        w.group = p.group;
+        w.group = CROSS ? p.group : NC;
         group = it / p.kv_heads;
         int64_t tiles = 0;  // of the whole batch
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         const int64_t n = min((int64_t)row_tiles - lo, run_end - run);
         w.row0 = rk.row0;
         w.ncol = CROSS ? rk.ncol : NC;
-        w.qrow0 = CROSS ? (int64_t)rk.qo0 * p.q_heads + w.kvh * p.group : (int64_t)w.b * p.q_heads + w.kvh * NC;
+        w.qrow0 = CROSS ? (int64_t)rk.qo0 * p.q_heads + w.kvh * p.group : 0;
         w.k0 = (int)lo * kKeys;
         w.count = (int)min((int64_t)rk.L - w.k0, n * kKeys);
         if (lane == 0 && w.kvh == 0) {  // for the merge: the runs that touch the row
