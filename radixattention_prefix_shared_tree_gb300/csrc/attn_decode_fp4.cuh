@@ -3,11 +3,14 @@
 //
 //   out[c] = sum_j softmax_j(scale q[c].K[j]) V[j],   K[j], V[j] = code * scale
 //
-// One warp per item (request, KV head, key chunk) with a private ring of
-// 32-key tiles in shared memory, filled by cp.async.  A key's row is 72 bytes
-// at D = 128 (64 of codes, 8 of scales) against 256 in bf16, so at HBM speed a
-// tile lasts half as many cycles per key as the bf16 pass has, and the pass is
-// bound by instruction issue as much as by HBM.  What that decides:
+// A warp works on one KV head and a stretch of 32-key tiles: whole rows (FUSED),
+// or an equal run of all rows' tiles laid end to end, whose parts
+// merge_runs_kernel joins.  The tiles come by cp.async into a two-stage ring,
+// four neighbouring heads' together where there are that many (COOP).  A key's
+// row is 72 bytes at D = 128 (64 of codes, 8 of scales) against 256 in bf16, so
+// HBM gives a tile fewer cycles than its instructions take: at 256 rows of
+// 512-5119 keys, 8 KV heads, the pass takes 166 us, its loads alone 131 and its
+// arithmetic alone 132; 123 would be HBM's copy rate.  What that decides:
 //  * code times scale is exactly an f16 value, so both products run on f16
 //    mma.sync with the values themselves and the softmax sees no scales;
 //  * the order of the head's dims inside the products is free as long as both
@@ -18,6 +21,8 @@
 //    interleaved before they are widened (half a logic instruction per pair
 //    instead of a byte permute each);
 //  * 32 keys per tile share one round of max shuffles and one rescale test.
+// Measured and left out at that size: a third stage 169 us, eight warps a CTA
+// 179, five or six CTAs per SM 211 and 251 (registers spill).
 #pragma once
 
 #include "attn_decode.cuh"
