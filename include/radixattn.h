@@ -303,7 +303,7 @@ rc_status bc_stats(bc_cache* cache, rc_stats_t* out);
  * bits (bias 15) and 3 mantissa bits, i.e. bits 14..7 of an f16.  An element's
  * value is its code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times its
  * block's scale, always an f16 value (so the queries of such a pool are taken
- * as f16 too: exact below 65504 in magnitude).  Scale byte 0xff is a NaN: its block's
+ * as f16 too: exact from 2^-17 to 65504 in magnitude, to 2^-25 below).  Scale byte 0xff is a NaN: its block's
  * elements are NaN, and a query row that reads them in K is NaN with lse
  * +infinity.  The four arrays are 16-byte aligned.  k_bscale and
  * v_bscale are read for such a pool only. */
@@ -327,7 +327,7 @@ typedef struct rc_pool_desc {
 typedef struct rc_attn_desc {
     rc_pool_desc pool;
     int32_t q_heads;   /* multiple of kv_heads; query head h reads kv head h / (q_heads/kv_heads) */
-    float sm_scale;    /* scale of q.k inside the softmax */
+    float sm_scale;    /* scale of q.k inside the softmax (attn_extend, the cascade, attn_cross: > 0) */
 } rc_attn_desc;
 
 /* Per-request slot tables on the device (caller-owned).  The keys of request b

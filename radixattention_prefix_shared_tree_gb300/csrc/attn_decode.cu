@@ -374,6 +374,9 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
         s = rc_host::check_fp4(P);
         if (s != RC_OK) return s;
         if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;
+        // the cascade takes the largest score for the largest scaled one; the
+        // table pass turns a negative scale into Q
+        if (use_casc ? !(desc->sm_scale > 0.f) : desc->sm_scale != desc->sm_scale) return RC_ERR_ARG;
     }
     const int G = desc->q_heads / P.kv_heads;
     unsigned char* w = static_cast<unsigned char*>(ws);

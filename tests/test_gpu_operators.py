@@ -305,6 +305,22 @@ def test_decode_fp4_vs_oracle(cuda, hq, hkv, d, lens):
         assert torch.equal(again, out[:B])
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_decode_fp4_scales_that_are_not_positive(cuda, scale):
+    """A negative scale prefers the smallest products; zero gives the keys' mean."""
+    hq, hkv, d, lens = 16, 4, 128, [1, 40, 333, 700]
+    pool = Pool("fp4", 2000, hkv, d, cuda, 21)
+    rows, table, start, length = tables(lens, 2000, 3, cuda)
+    q = rand(torch.Generator().manual_seed(2), len(lens), hq, d)
+    desc = ra.make_attn_desc(pool.desc, hq, scale)
+    ws = torch.empty(max(ra.attn_decode_workspace(desc, len(lens), 700), 256), dtype=torch.uint8, device=cuda)
+    out, lse = torch.empty_like(q), torch.empty(len(lens), hq, dtype=torch.float32, device=cuda)
+    ra.attn_decode(desc, q, ra.make_kv_table(table, start, length, 700), len(lens), out, lse, ws)
+    assert ra.rc_sync(pool.err) == ra.RC_OK
+    k, v = pool.values()
+    check(out, lse, f4.attention(f32(q).astype(np.float64), k, v, rows, hq, hkv, float(np.float32(scale))), pool.u_p)
+
+
 def test_decode_fp4_large_and_small_values(cuda):
     """Rows spread over e^(+-6) in size: peaked softmax, outputs of many units (the mean bar grows with them)."""
     hq, hkv, d, lens = 32, 8, 128, [1, 40, 333, 2049]

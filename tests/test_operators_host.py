@@ -183,15 +183,15 @@ def test_fp4_pool_refused_where_unsupported(built):
     buf = torch.zeros(1 << 14, dtype=BF)
     b = (buf.data_ptr() + 255) // 256 * 256
 
-    def decode(pool, k_new=None, q=b, hq=32, out=None):
-        d = ra.make_attn_desc(pool, hq, 0.1)
+    def decode(pool, k_new=None, q=b, hq=32, out=None, scale=0.1, casc=None):
+        d = ra.make_attn_desc(pool, hq, scale)
         kv = ra.rc_kv_table(slots=b, start=b, len=b, max_len=16, table_len=64)
         if k_new:
             return L.attn_decode_append(C.byref(d), q, k_new, k_new, C.byref(kv), 2, None, b, None, b, 1 << 24, None)
-        return L.attn_decode(C.byref(d), q, C.byref(kv), 2, None, out or b, None, b, 1 << 24, None)
+        return L.attn_decode(C.byref(d), q, C.byref(kv), 2, casc, out or b, None, b, 1 << 24, None)
 
-    def extend(pool, q=b, hq=32):
-        d = ra.make_attn_desc(pool, hq, 0.1)
+    def extend(pool, q=b, hq=32, scale=0.1):
+        d = ra.make_attn_desc(pool, hq, scale)
         kv = ra.rc_kv_table(slots=b, start=b, len=b, max_len=16, table_len=64)
         return L.attn_extend(C.byref(d), q, b, C.byref(kv), 2, 8, b, None, None, 0, None)
 
@@ -201,6 +201,12 @@ def test_fp4_pool_refused_where_unsupported(built):
     odd.v_bscale = odd.v_bscale + 8
     for call in (decode, extend, store):
         assert call(no_scale) == A and call(odd) == A and call(deep) == U, call
+    casc = ra.rc_cascade(n_seg=1, total_seg_rows=2, max_seg_rows=2, max_seg_len=8, seg_slots=b, seg_indptr=b,
+                         seg_row_indptr=b, seg_rows=b, req_seg_indptr=b, req_seg_pos=b)
+    nan = float("nan")
+    for scale in (0.0, -0.1, nan):
+        assert extend(fp4_pool(), scale=scale) == A and decode(fp4_pool(), scale=scale, casc=C.byref(casc)) == A
+    assert decode(fp4_pool(), scale=nan) == A
     empty = fp4_pool()
     empty.n_slots = 0
     assert decode(empty) == A and extend(empty) == A and store(empty) == A
