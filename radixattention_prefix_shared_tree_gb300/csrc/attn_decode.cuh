@@ -69,10 +69,10 @@ struct Item {
     int b, kvh, chunk, ncol, L, k0, count;
     int64_t row0;        // the row's first entry in the table
     int64_t qrow0;       // CROSS: flat (token, head) row of column 0
-    int q_heads, group;
-    template <bool CROSS>
-    RC_DEV int64_t qrow(int c) const {
-        return CROSS ? qrow0 + (int64_t)(c / group) * q_heads + c % group : (int64_t)b * q_heads + kvh * group + c;
+    template <int NC, bool CROSS>
+    RC_DEV int64_t qrow(const DecParams& p, int c) const {  // column c's
+        return CROSS ? qrow0 + (int64_t)(c / p.group) * p.q_heads + c % p.group
+                     : (int64_t)b * p.q_heads + kvh * NC + c;
     }
 };
 
@@ -87,8 +87,6 @@ RC_DEV Item decode_item(const DecParams& p, int it, int lane) {
     w.b = rest / p.n_chunks;
     w.row0 = p.start[w.b];
     w.L = p.len[w.b];
-    w.q_heads = p.q_heads;
-    w.group = CROSS ? p.group : NC;
     bool bad = w.row0 < 0 || w.L < 0 || w.row0 + w.L > p.table_len;
     if constexpr (CROSS) {
         const int qo0 = p.qo_indptr[w.b], nq = p.qo_indptr[w.b + 1] - qo0;
@@ -143,10 +141,10 @@ RC_DEV RowKeys row_keys(const DecParams& p, int b) {
 
 // A split item without keys: decode leaves its partial unwritten (the merge
 // goes by the row's length), cross marks its columns' partials empty.
-template <bool CROSS>
+template <int NC, bool CROSS>
 RC_DEV void empty_partial(const DecParams& p, const Item& w, int lane) {
     if constexpr (CROSS)
-        if (lane < w.ncol) p.part_lse[w.qrow<CROSS>(lane) * p.n_chunks + w.chunk] = -INFINITY;
+        if (lane < w.ncol) p.part_lse[w.qrow<NC, CROSS>(p, lane) * p.n_chunks + w.chunk] = -INFINITY;
 }
 
 // The cascade partials a row folds in: entries e0.. of req_seg_pos, n_parts
@@ -178,7 +176,7 @@ RC_DEV void decode_epilogue(const DecParams& p, const Item& w, float* sE, float*
     grid_dep_wait();
     if constexpr (!FUSED) {
         for (int h = 0; h < w.ncol; ++h) {
-            const int64_t idx = w.qrow<CROSS>(h) * p.n_chunks + w.chunk;
+            const int64_t idx = w.qrow<NC, CROSS>(p, h) * p.n_chunks + w.chunk;
             for (int d = lane; d < D; d += 32) p.part_o[idx * D + d] = sE[h * D + d];
             if (lane == 0) p.part_lse[idx] = sOwn[h];
         }
@@ -244,7 +242,7 @@ RC_DEV void decode_epilogue(const DecParams& p, const Item& w, float* sE, float*
 #pragma unroll
         for (int h = 0; h < NC; ++h) {
             if (CROSS && h >= w.ncol) break;
-            const int64_t orow = w.qrow<CROSS>(h);
+            const int64_t orow = w.qrow<NC, CROSS>(p, h);
             const float inv = w_h[h] > 0.f ? 1.f / w_h[h] : 0.f;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)

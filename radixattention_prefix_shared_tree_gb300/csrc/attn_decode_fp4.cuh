@@ -150,8 +150,6 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
         first_row = seg.row(p, lane);
     } else {
         w.kvh = it % p.kv_heads;
-        w.q_heads = p.q_heads;
-        w.group = CROSS ? p.group : NC;
         group = it / p.kv_heads;
         int64_t tiles = 0;  // of the whole batch
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -283,7 +281,7 @@ __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_
     {
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const bool hv = g_lane < w.ncol;
-        const uint4* qrow = reinterpret_cast<const uint4*>(p.q + w.qrow<CROSS>(hv ? g_lane : 0) * D + t_lane * (D / 4));
+        const uint4* qrow = reinterpret_cast<const uint4*>(p.q + w.qrow<NC, CROSS>(p, hv ? g_lane : 0) * D + t_lane * (D / 4));
 #pragma unroll
         for (int j = 0; j < KS / 2; ++j) {
             uint4 x = hv ? __ldg(qrow + j) : make_uint4(0, 0, 0, 0);

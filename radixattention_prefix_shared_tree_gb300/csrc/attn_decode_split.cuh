@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
     }
     if (!FUSED && count == 0) {
         grid_dep_wait();
-        empty_partial<CROSS>(p, w, lane);
+        empty_partial<G, CROSS>(p, w, lane);
         return;
     }
     const int32_t* keys = p.table + w.row0 + k0;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
     uint32_t qb[KS][2];
     {
         const bool hv = g_lane < (CROSS ? w.ncol : G);
-        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.q + w.qrow<CROSS>(hv ? g_lane : 0) * D);
+        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.q + w.qrow<G, CROSS>(p, hv ? g_lane : 0) * D);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             if constexpr (FP8) {
