@@ -53,7 +53,7 @@ constexpr int Q_BYTES = M * (DK - QT) * 2;
 constexpr int TILE_BYTES = TN * DK * 2;
 constexpr uint32_t SB = CK * 128;   // bytes between 8-row groups of a tile
 constexpr uint32_t SBQ = CQ * 128;  // bytes between 8-head groups of Q
-constexpr int kBars = 1 + 2 * NS + 2 + 2 + 1;
+constexpr int kBars = 1 + 2 * NS + 2 + 2 + 1 + 1;
 constexpr uint32_t kWaitIter = 1u << 24;
 static_assert(COL_Q + QT / 2 <= COL_O, "Q and the S buffers overlap O in TMEM");
 
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(THREADS, 1) mla_tc_kernel(const Params p) {
     uint64_t* s_full = bar + 1 + 2 * NS;           // [2], count 1
     uint64_t* p_full = s_full + 2;                 // [2], count 4
     uint64_t* o_done = p_full + 2;                 // count 1 per tile
+    uint64_t* drained = o_done + 1;                // count 1: products in flight when a wait gave up
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1) mla_tc_kernel(const Params p) {
             tc::mbar_init(&p_full[i], 4);
         }
         tc::mbar_init(o_done, 1);
+        tc::mbar_init(drained, 1);
         tc::fence_mbar_init();
     }
     if (warp == W_MMA) {
@@ -387,7 +389,9 @@ __global__ void __launch_bounds__(THREADS, 1) mla_tc_kernel(const Params p) {
                     tc::mma_bf16_ts_h(tbase + COL_O, tbase + (t & 1) * TN + j * 8, vd.lo + j * (2 * SB / 16), vd.hi,
                                       idPV, (t > 0 || j > 0) ? 1u : 0u);
                 tc::commit(o_done);
-                tc::commit(&kv_empty[s]);
+                // a stage's last use has nobody to tell, and the CTA, which
+                // leaves on o_done, must not leave an arrival behind
+                if (t + NS < n_tiles) tc::commit(&kv_empty[s]);
                 ++t;
                 moved = true;
             }
@@ -412,7 +416,11 @@ __global__ void __launch_bounds__(THREADS, 1) mla_tc_kernel(const Params p) {
                 else if (now - t0 > tc::kWaitNs || idle >= kWaitIter) ok = false;
             }
         }
-        if (!ok) rc::flag_error(p.err, rc::kErrTimeout);
+        if (!ok) {
+            rc::flag_error(p.err, rc::kErrTimeout);
+            tc::commit(drained);
+            tc::mbar_wait(drained, 0, kWaitIter);  // the products read stages and write TMEM
+        }
     }
     tc::fence_before();
     __syncthreads();
