@@ -129,17 +129,19 @@ struct Fp4Feed {
     // chunk c of row r lies at chunk c ^ swz(r): eight rows' equal chunks then
     // touch every bank once
     RC_DEV static int swz(int r) { return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1; }
-    // lane r: the slot id of row r's key (-1: none)
-    RC_DEV int id_of(int t) const {
-        const int key = t * TN + key_of(lane);
-        return lane < RAW_ROWS && key_of(lane) < TN && t < n_tiles && key < key_count ? __ldg(keys + key) : -1;
+    // whether row `lane` of this warp's part of tile t is a key (none of a tile past the last)
+    RC_DEV bool has(int t) const {
+        return lane < RAW_ROWS && key_of(lane) < TN && t * TN + key_of(lane) < key_count;
     }
+    // lane r: the slot id of row r's key (-1 where there is none, which `has`
+    // tells apart from a table entry of -1)
+    RC_DEV int id_of(int t) const { return has(t) ? __ldg(keys + t * TN + key_of(lane)) : -1; }
     RC_DEV void fetch(int t, int id) const {
         if (t < n_tiles) {
             const uint32_t dst = rc::smem_u32(raw) + (t % RAW) * raw_bytes<D>();
             const int c = lane % CPR;
             const bool live = (uint32_t)id < n_slots;
-            if (!live && id != -1) rc::flag_error(p.err, rc::kErrBadSlot);
+            if (!live && has(t)) rc::flag_error(p.err, rc::kErrBadSlot);
             const int safe = live ? id : 0;
 #pragma unroll
             for (int i = 0; i < (RAW_ROWS + RPI - 1) / RPI; ++i) {
