@@ -450,7 +450,10 @@ rc_status attn_decode_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
  *   out[b][h] = sum_j softmax_j(sm_scale * q[b][h].K[j][g(h)]) V[j][g(h)]
  * over the cascade segments of row b (if any) and then its table row.
  * out: [batch][q_heads][head_dim_v] bf16.  lse: NULL or [batch][q_heads] fp32,
- * natural log of the softmax denominator.  ws: attn_decode_workspace bytes.
+ * natural log of the softmax denominator.  A NaN in a key makes the output
+ * of every (row, head) that reads it NaN with an lse of +infinity, in all
+ * attention calls, however the row's keys are divided; a row without keys
+ * gives zeros and an lse of -infinity.  ws: attn_decode_workspace bytes.
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED (head layout), RC_ERR_CUDA. */
 rc_status attn_decode(const rc_attn_desc* desc, const void* q, const rc_kv_table* kv,
                       int32_t batch, const rc_cascade* cascade, void* out, float* lse,

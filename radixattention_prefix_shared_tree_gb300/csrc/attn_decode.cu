@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32) merge_kernel(const float* __restrict__ tai
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) out[(int64_t)bh * D + lane + 32 * j] = __float2bfloat16_rn(acc[j] * inv);
-    if (lse && lane == 0) lse[bh] = wsum > 0.f ? (m + log2f(wsum)) * rc::kLn2 : -INFINITY;
+    if (lse && lane == 0) lse[bh] = rc::log2_sum(m, wsum) * rc::kLn2;
 }
 
 // ------------------------------------------------------------------ planning

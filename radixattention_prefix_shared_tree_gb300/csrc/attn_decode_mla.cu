@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(128, 2) mla_decode_kernel(const Params p) {
 
     const float inv0 = l_run[0] > 0.f ? 1.f / l_run[0] : 0.f;
     const float inv1 = l_run[1] > 0.f ? 1.f / l_run[1] : 0.f;
-    const float lse0 = l_run[0] > 0.f ? m_run[0] + log2f(l_run[0]) : -INFINITY;
-    const float lse1 = l_run[1] > 0.f ? m_run[1] + log2f(l_run[1]) : -INFINITY;
+    const float lse0 = rc::log2_sum(m_run[0], l_run[0]);
+    const float lse1 = rc::log2_sum(m_run[1], l_run[1]);
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
         const int head = hb * HB + g_lane + 8 * hr;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(32) mla_merge_kernel(const Params p) {
     const float inv = w > 0.f ? 1.f / w : 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) p.out[(int64_t)bh * DV + lane + 32 * j] = __float2bfloat16_rn(acc[j] * inv);
-    if (p.lse && lane == 0) p.lse[bh] = w > 0.f ? (m + log2f(w)) * rc::kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[bh] = rc::log2_sum(m, w) * rc::kLn2;
 }
 
 }  // namespace rc_mla

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1) mla_tc_kernel(const Params p) {
         // warp's 32x32 fp32 blocks go through its 4 KB of the (now free) Q
         // region, so stores write whole row segments.
         const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-        const float lse2 = l_run > 0.f ? m_used + log2f(l_run) : -INFINITY;
+        const float lse2 = rc::log2_sum(m_used, l_run);
         float* stg = reinterpret_cast<float*>(sQ + warp * 4096);
         const int k8 = lane & 7;
 #pragma unroll 1

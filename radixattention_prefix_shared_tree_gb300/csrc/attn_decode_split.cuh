@@ -333,13 +333,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
         sE[(2 * t_lane + 1) * D + d1] = o[mt][3] * inv1;
     }
     if (g_lane == 0) {
-        if constexpr (CROSS) {
-            sOwn[2 * t_lane] = rc::log2_sum(m_run[0], l_run[0]);
-            sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1], l_run[1]);
-        } else {
-            sOwn[2 * t_lane] = l_run[0] > 0.f ? m_run[0] + log2f(l_run[0]) : -INFINITY;
-            sOwn[2 * t_lane + 1] = l_run[1] > 0.f ? m_run[1] + log2f(l_run[1]) : -INFINITY;
-        }
+        sOwn[2 * t_lane] = rc::log2_sum(m_run[0], l_run[0]);
+        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1], l_run[1]);
     }
     __syncwarp();
     decode_epilogue<D, G, FUSED, CROSS>(p, w, sE, sOwn, seg, first_row, lane);

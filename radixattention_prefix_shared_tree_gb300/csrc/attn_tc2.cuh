@@ -706,9 +706,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         // instruction would touch 32 rows, one tag each: 2.6 us a CTA.)
         if (q < n_qt) {
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            const float lse2 = FP4 || MODE == rc::MQMode::kCross ? rc::log2_sum(m_used, l_run)
-                               : l_run > 0.f                     ? m_used + log2f(l_run)
-                                                                 : -INFINITY;
+            const float lse2 = rc::log2_sum(m_used, l_run);
             const bool whole = MODE != rc::MQMode::kCascade && p.seg_chunks == 1;
             unsigned char* stg = sQ + warp * 32 * D * 2;
             // n 16-byte chunks of every row of the warp, staged, to row `rw` of dst
