@@ -294,7 +294,12 @@ rc_status bc_stats(bc_cache* cache, rc_stats_t* out);
  * group]: k and v hold E4M3 codes, one byte per element in the same
  * [n_slots][kv_heads][head_dim] layout, and k_scale / v_scale are fp32
  * [n_slots][kv_heads]; an element's value is its code times the scale of its
- * (slot, head) row.  kv_store quantises (see there); attn_decode reads it.
+ * (slot, head) row.  kv_store quantises (see there); every attention call
+ * reads it.  The softmax weights (relative to the largest, or within 2^8 of it)
+ * times the V scales are rounded to f16, taken relative to the largest V scale
+ * read so far: for V scales from 2^-94 to 2^106 each product keeps f16's 11 bits
+ * unless it is below 2^-16 of that scale.  The queries are taken as f16 (exact
+ * from 2^-17 to 65504 in magnitude, to 2^-25 below, infinite above).
  * 4-bit pool (kv_fp8 == RC_KV_FP4; GQA, head_dim 64 or 128; a library extra):
  * a (slot, head) row of head_dim values is head_dim/16 blocks of 16.  k and v
  * hold E2M1 codes, two per byte, the even element in the low half:

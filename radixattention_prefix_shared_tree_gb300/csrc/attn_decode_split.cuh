@@ -180,6 +180,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // FP8: O and l are in units of 2^unit_f (rc::scale_unit), until a V scale of
+    // unit_limit or more
+    float unit_f = rc::kUnitMin, unit_limit = rc::pow2(rc::kUnitMin + 6);
 
     for (int t = 0; t < n_tiles; ++t) {
         rc::cp_async_wait<S - 1>();  // tile t landed (later tiles may still be in flight)
@@ -239,6 +242,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
         float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
         float alpha[2] = {1.f, 1.f};
         bool grow = false;
+        float vs_lo = 0.f, vs_hi = 0.f;  // FP8: V scales of keys g and g+8
+        if constexpr (FP8) {
+            vs_lo = sSc[kWarpKeys + g_lane], vs_hi = sSc[kWarpKeys + g_lane + 8];
+            grow = fmaxf(fabsf(vs_lo), fabsf(vs_hi)) >= unit_limit;
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
@@ -250,13 +258,23 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
                 grow = true;
             }
         }
-        const float mu0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float mu1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
-        const float p0 = rc::fast_exp2(s[0] - mu0), p1 = rc::fast_exp2(s[1] - mu1);
-        const float p2 = rc::fast_exp2(s[2] - mu0), p3 = rc::fast_exp2(s[3] - mu1);
+        const float mu0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) + (FP8 ? unit_f : 0.f);
+        const float mu1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) + (FP8 ? unit_f : 0.f);
+        float p0 = rc::fast_exp2(s[0] - mu0), p1 = rc::fast_exp2(s[1] - mu1);
+        float p2 = rc::fast_exp2(s[2] - mu0), p3 = rc::fast_exp2(s[3] - mu1);
         if (__any_sync(0xffffffffu, grow)) {
             l_run[0] *= alpha[0];
             l_run[1] *= alpha[1];
+            if constexpr (FP8) {
+                const int unit = (int)unit_f, u = rc::scale_unit(__reduce_max_sync(
+                                                  0xffffffffu, max(rc::abs_bits(vs_lo), rc::abs_bits(vs_hi))));
+                if (u > unit) {
+                    for (float* x : {&l_run[0], &l_run[1], &alpha[0], &alpha[1], &p0, &p1, &p2, &p3})
+                        *x = rc::to_unit(*x, unit, u);
+                    unit_f = (float)u;
+                    unit_limit = rc::pow2(u + 6);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 o[i][0] *= alpha[0];
@@ -273,9 +291,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
             // 2t, 2t+1, 2t+8, 2t+9 (dims 16g..16g+15); product mt uses dims
             // 16g+2mt (row g) and 16g+2mt+1 (row g+8), paired across keys
             // with a byte permute
-            const float v_lo = sSc[kWarpKeys + g_lane], v_hi = sSc[kWarpKeys + g_lane + 8];
-            const uint32_t pb0 = rc::movmatrix_trans(rc::pack_f16(p0 * v_lo, p1 * v_lo));
-            const uint32_t pb1 = rc::movmatrix_trans(rc::pack_f16(p2 * v_hi, p3 * v_hi));
+            const uint32_t pb0 = rc::movmatrix_trans(rc::pack_f16(p0 * vs_lo, p1 * vs_lo));
+            const uint32_t pb1 = rc::movmatrix_trans(rc::pack_f16(p2 * vs_hi, p3 * vs_hi));
             const uint4 w0 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane, g_lane));
             const uint4 w1 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane + 1, g_lane));
             const uint4 w8 = *reinterpret_cast<const uint4*>(sV + rc::swz<CH>(2 * t_lane + 8, g_lane));
@@ -333,8 +350,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
         sE[(2 * t_lane + 1) * D + d1] = o[mt][3] * inv1;
     }
     if (g_lane == 0) {
-        sOwn[2 * t_lane] = rc::log2_sum(m_run[0], l_run[0]);
-        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1], l_run[1]);
+        const float back = FP8 ? unit_f : 0.f;
+        sOwn[2 * t_lane] = rc::log2_sum(m_run[0] + back, l_run[0]);
+        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1] + back, l_run[1]);
     }
     __syncwarp();
     decode_epilogue<D, G, FUSED, CROSS>(p, w, sE, sOwn, seg, first_row, lane);

@@ -38,8 +38,9 @@
 // loads, widen them to f16 in registers and store the operand tiles
 // themselves (then fence to the async proxy and arrive), along with the
 // tile's 64 K and 64 V scales; the softmax scales S by the K scales and folds
-// the V scales into P.  The ring has 4 stages (the scales take the room of
-// the fifth).
+// the V scales into P, against a reference that keeps the products within f16's
+// normal numbers (rc::scale_unit).  The ring has 4 stages (the scales take the
+// room of the fifth).
 //
 // 4-bit pool (E2M1 codes, one scale byte per 16 of them): code times scale is
 // itself an f16 value, so the stages hold the pool's exact values and the
@@ -91,7 +92,7 @@ constexpr int RAW = 2;
 template <int D, int FMT = rc::kFmtBf16>
 __host__ __device__ constexpr int smem_bytes() {
     return QT * TM * D * 2 + stages<FMT>() * 2 * TN * D * 2 +
-           (FMT == rc::kFmtFp8   ? stages<FMT>() * 2 * TN * 4
+           (FMT == rc::kFmtFp8   ? stages<FMT>() * (2 * TN + 1) * 4
             : FMT == rc::kFmtFp4 ? producers<FMT>() * RAW * raw_bytes<D>()
                                  : 0) +
            n_bars<FMT>() * 8 + 16;
@@ -216,9 +217,10 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
     unsigned char* sQ = smem;                                  // [QT][128 rows][D]
     unsigned char* sKV = sQ + QT * TM * D * 2;                 // [NS][K, V]
     float* sScale = reinterpret_cast<float*>(sKV + NS * 2 * KV_BYTES);  // FP8: [NS][K scales, V scales]
+    float* sUnit = sScale + NS * 2 * TN;                                 // FP8: [NS] the unit of the V scales
     unsigned char* sRaw = sKV + NS * 2 * KV_BYTES;                       // FP4: [NP][RAW] tiles of codes and scales
     uint64_t* bar = reinterpret_cast<uint64_t*>(sKV + NS * 2 * KV_BYTES +
-                                                (FP8 ? NS * 2 * TN * 4 : FP4 ? NP * RAW * raw_bytes<D>() : 0));
+                                                (FP8 ? NS * (2 * TN + 1) * 4 : FP4 ? NP * RAW * raw_bytes<D>() : 0));
     uint64_t* q_full = bar + 0;              // count 8 (softmax warps)
     uint64_t* kv_full = bar + 1;             // [NS], count 32 (the lanes of the tile's producer warp; FP4: of all)
     uint64_t* kv_empty = bar + 1 + NS;       // [NS], count 1 (MMA commit)
@@ -588,6 +590,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         else lim = row_valid ? key_count : 0;
         const float sc = p.scale_log2;
         float m_used = -INFINITY, l_run = 0.f;
+        float unit = 0.f;  // FP8: O and l are in units of 2^unit (rc::scale_unit)
         if (q < n_qt) {
             for (int t = 0; t < n_tiles && ok; ++t) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[q * 2 + (t & 1)], (t >> 1) & 1, kWaitIter));
@@ -605,12 +608,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     s[32 + j] = __uint_as_float(sb[j]);
                 }
                 const float* tsc = sScale + (t % NS) * 2 * TN;  // FP8: this tile's K then V scales
+                float u = 0.f;                                  // and their unit
                 if constexpr (FP8) {
                     // the producer's scale stores are visible once its arrival
                     // on the stage is (that phase completed before S(t) ran)
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[t % NS], (t / NS) & 1, kWaitIter)) && ok;
 #pragma unroll
                     for (int j = 0; j < TN; ++j) s[j] *= tsc[j];
+                    u = sUnit[t % NS];
+                    if (t == 0) unit = u;
                 }
                 const int kb = t * TN;
                 if (kb + TN > lim) {  // the causal edge or the end of the keys
@@ -630,11 +636,17 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                 const float mt = mraw * sc;  // sc > 0: the max of the scaled row
                 const bool grow = mt > m_used + 8.f;
                 const bool rescale_o = grow && m_used != -INFINITY;
-                if (__any_sync(0xffffffffu, rescale_o)) {
+                const bool larger = FP8 && u > unit;  // all rows alike: a tile of a larger unit than O's
+                if (larger || __any_sync(0xffffffffu, rescale_o)) {
                     // O must be stable: the previous tile's P.V has completed
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&o_done[q], (t - 1) & 1, kWaitIter)) && ok;
                     tc::fence_after();
-                    const float a = rescale_o ? ex2(m_used - mt) : 1.f;
+                    float a = rescale_o ? ex2(m_used - mt) : 1.f;
+                    if (larger) {
+                        a = rc::to_unit(a, (int)unit, (int)u);
+                        l_run = rc::to_unit(l_run, (int)unit, (int)u);
+                        unit = u;
+                    }
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
@@ -650,7 +662,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     l_run *= ex2(m_used - mt);  // 0 while nothing was seen
                     m_used = mt;
                 }
-                const float nmu = m_used == -INFINITY ? 0.f : -m_used;
+                const float nmu = (m_used == -INFINITY ? 0.f : -m_used) - (FP8 ? unit : 0.f);
                 uint32_t pk[32];
                 float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -706,7 +718,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
         // instruction would touch 32 rows, one tag each: 2.6 us a CTA.)
         if (q < n_qt) {
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            const float lse2 = rc::log2_sum(m_used, l_run);
+            const float lse2 = rc::log2_sum(FP8 ? m_used + unit : m_used, l_run);
             const bool whole = MODE != rc::MQMode::kCascade && p.seg_chunks == 1;
             unsigned char* stg = sQ + warp * 32 * D * 2;
             // n 16-byte chunks of every row of the warp, staged, to row `rw` of dst
@@ -847,6 +859,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     }
                 }
                 float* tsc = sScale + s * 2 * TN;
+                uint32_t top = 0;  // the bits of the largest V scale
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                     const int key = lane + 32 * h2;
@@ -854,8 +867,12 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     const bool live = t * TN + key < key_count && slot >= 0 && (int64_t)slot < p.n_slots;
                     const int64_t row = (int64_t)(live ? slot : 0) * p.kv_heads + kvh;
                     tsc[key] = live ? __ldg(p.k_scale + row) : 0.f;
-                    tsc[TN + key] = live ? __ldg(p.v_scale + row) : 0.f;
+                    const float vs = live ? __ldg(p.v_scale + row) : 0.f;
+                    tsc[TN + key] = vs;
+                    top = max(top, rc::abs_bits(vs));
                 }
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (lane == 0) sUnit[s] = (float)rc::scale_unit(top);
                 tc::fence_proxy_async();  // this lane's stores, before the tensor core reads them
                 mbar_arrive(&kv_full[s]);
             }

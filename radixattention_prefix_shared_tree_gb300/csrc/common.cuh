@@ -221,6 +221,30 @@ RC_DEV float fast_exp2(float x) { return exp2f(x); }
 // so that a merge turns the row into NaN instead of leaving the part out.
 RC_DEV float log2_sum(float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; }
 
+// 2^e for -126 <= e <= 127.
+RC_DEV float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// E4M3 pools: the softmax weights times the keys' V scales enter P.V in f16,
+// whose normal numbers span 2^-14 to 2^16, while a V scale can be nearly any
+// fp32.  So the exponentials' reference carries a unit beside the running
+// maximum m: weights are 2^(s - m - unit), their sum and O are both in units of
+// 2^unit, and it cancels in O / l.  The unit is a multiple of 4 that puts the
+// largest V scale so far at 2^2 or above and below 2^6 (in steps of four,
+// because ordinary scales then keep one unit).  With weights of at most 2^8 (m
+// is lazy) the products stay below 2^14, and one keeps all its bits down to
+// 2^-16 of the largest scale; below, 2^-25 of the unit is lost.  -96..100, so
+// that l stays an fp32: V scales from 2^-94 to 2^106.
+constexpr int kUnitMin = -96, kUnitMax = 100;
+RC_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+RC_DEV int scale_unit(uint32_t largest_abs_bits) {
+    return max(kUnitMin, min(kUnitMax, ((int)(largest_abs_bits >> 23) - 129) & ~3));
+}
+// x in units of 2^from, in units of 2^to (from <= to).
+RC_DEV float to_unit(float x, int from, int to) {
+    const int half = (from - to) / 2;
+    return x * pow2(half) * pow2(from - to - half);
+}
+
 // Byte offset of 16-byte chunk `c` of row `r` in a tile whose rows are
 // `chunks` 16-byte chunks long, XOR-swizzled on the low three bits so that
 // ldmatrix over 8 consecutive rows touches 8 different bank groups.
