@@ -444,7 +444,9 @@ typedef struct rc_cascade {
     const int32_t* host_seg_row_indptr;
 } rc_cascade;
 
-/* Workspace bytes attn_decode needs for this batch (split partials). */
+/* Workspace bytes attn_decode needs for this batch (split partials) and any
+ * max_len up to the given one.  Another batch or cascade may need more, a
+ * smaller batch too. */
 rc_status attn_decode_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_len,
                                 const rc_cascade* cascade, size_t* bytes);
 
@@ -549,8 +551,9 @@ rc_status attn_decode_static(const rc_attn_desc* desc, const void* q, const rc_k
                              rc_stream_t stream);
 
 /* Workspace bytes with which attn_extend splits long rows of a small batch over
- * more CTAs (4-bit pools; 0 for the others, and where splitting gains nothing).
- * Without that workspace it computes the same rows unsplit. */
+ * more CTAs (4-bit pools; 0 for the others, and where splitting gains nothing),
+ * for this batch and max_q and any max_len up to the given one.  Without that
+ * workspace it computes the same rows unsplit. */
 rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
                                 int32_t max_len, size_t* bytes);
 
@@ -569,7 +572,9 @@ rc_status attn_extend(const rc_attn_desc* desc, const void* q, const int32_t* qo
                       const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out,
                       float* lse, void* ws, size_t ws_bytes, rc_stream_t stream);
 
-/* Workspace bytes attn_cross needs for this batch (0 unless keys are split). */
+/* Workspace bytes attn_cross needs for this batch and max_q and any max_len up to
+ * the given one (0 unless keys are split).  Another batch or max_q, a smaller
+ * one too, may need more: its keys can be divided otherwise. */
 rc_status attn_cross_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
                                int32_t max_len, size_t* bytes);
 

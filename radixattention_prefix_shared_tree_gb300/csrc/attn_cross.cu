@@ -72,7 +72,9 @@ rc_status plan_cross(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_
         pl->part_lse = align256(parts * sizeof(float));
         pl->row_runs = align256((size_t)batch * 2 * sizeof(int32_t));
     } else if (pl->n_chunks > 1) {
-        const size_t rows = (size_t)batch * max_q * d->q_heads * pl->n_chunks;
+        // room for `splits` chunks, which some max_len up to this one has:
+        // n_chunks, after rounding, falls as max_len passes a unit
+        const size_t rows = (size_t)batch * max_q * d->q_heads * splits;
         pl->part_o = align256(rows * P.head_dim_v * sizeof(float));
         pl->part_lse = align256(rows * sizeof(float));
     }

@@ -128,6 +128,7 @@ struct DecodePlan {
     int seg_chunk = 0, seg_chunks = 0;  // cascade: keys per CTA, CTAs per segment
     bool fused = false;                 // one CTA per (row, KV head): no merge pass
     size_t tail_o = 0, tail_lse = 0, row_runs = 0, seg_o = 0, seg_lse = 0, total = 0;
+    size_t bound = 0;                   // the largest total of any max_len up to this one
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -201,7 +202,15 @@ rc_status plan_decode(const rc_attn_desc* d, int32_t batch, int32_t max_len, con
     pl->seg_o = align256(srows * dv * sizeof(float));
     pl->seg_lse = align256(srows * sizeof(float));
     pl->total = pl->tail_o + pl->tail_lse + pl->row_runs + pl->seg_o + pl->seg_lse;
+    // Chunks are rounded up to kDecKeys keys, so n_chunks can fall as max_len
+    // grows; `splits`, which it reaches at some max_len up to this one, cannot.
+    // (A 4-bit pool's runs only grow.)
+    pl->bound = pl->total;
+    if (!is_fp4 && !pl->fused)
+        pl->bound += align256(rows * splits * dv * sizeof(float)) - pl->tail_o +
+                     align256(rows * splits * sizeof(float)) - pl->tail_lse;
     if (pl->total == 0) pl->total = 256;
+    if (pl->bound == 0) pl->bound = 256;
     return RC_OK;
 }
 
@@ -324,13 +333,13 @@ extern "C" rc_status attn_decode_workspace(const rc_attn_desc* desc, int32_t bat
     if (desc && desc->pool.mla) {
         if (batch < 0 || max_len < 0 || desc->q_heads <= 0) return RC_ERR_ARG;
         if (cascade && cascade->n_seg > 0) return RC_ERR_UNSUPPORTED;
-        *bytes = rc_host::mla_workspace(batch, desc->q_heads, max_len);
+        *bytes = rc_host::mla_workspace_bound(batch, desc->q_heads, max_len);
         return RC_OK;
     }
     DecodePlan pl;
     rc_status s = plan_decode(desc, batch, max_len, cascade, &pl);
     if (s != RC_OK) return s;
-    *bytes = pl.total;
+    *bytes = pl.bound;
     return RC_OK;
 }
 
@@ -580,9 +589,18 @@ extern "C" rc_status attn_decode_static(const rc_attn_desc* desc, const void* q,
     if (!desc || !kv || batch < 0) return RC_ERR_ARG;
     if (batch == 0) return RC_OK;
     const rc_cascade* cc = casc && casc->n_seg > 0 ? casc : nullptr;  // as attn_decode plans it
-    size_t need = 0;
-    rc_status s = attn_decode_workspace(desc, batch, kv->max_len, cc, &need);
-    if (s != RC_OK) return s;
+    size_t need = 0;  // of this very call, not of every smaller max_len
+    rc_status s = RC_OK;
+    if (desc->pool.mla) {
+        if (kv->max_len < 0 || desc->q_heads <= 0) return RC_ERR_ARG;
+        if (cc) return RC_ERR_UNSUPPORTED;
+        need = rc_host::mla_workspace(batch, desc->q_heads, kv->max_len);
+    } else {
+        DecodePlan pl;
+        s = plan_decode(desc, batch, kv->max_len, cc, &pl);
+        if (s != RC_OK) return s;
+        need = pl.total;
+    }
     if (need > (size_t)RC_STATIC_SCRATCH_BYTES) return RC_ERR_SCRATCH;
     void* ws = nullptr;
     s = scratch_for_current_device(&ws);

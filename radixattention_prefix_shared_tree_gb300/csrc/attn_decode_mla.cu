@@ -321,13 +321,43 @@ void mla_plan(int32_t batch, int32_t q_heads, int32_t max_len, int* chunk, int* 
     *n_chunks = max_len > 0 ? (int)((max_len + c - 1) / c) : 1;
 }
 
-size_t mla_workspace(int32_t batch, int32_t q_heads, int32_t max_len) {
-    int chunk = 0, nc = 0;
-    mla_plan(batch, q_heads, max_len, &chunk, &nc);
+size_t mla_partials(int32_t batch, int32_t q_heads, int64_t nc) {
     if (nc <= 1) return 256;
     const size_t rows = (size_t)batch * q_heads * nc;
     const size_t a = (rows * rc_mla::DV * sizeof(float) + 255) & ~size_t(255);
     return a + ((rows * sizeof(float) + 255) & ~size_t(255));
+}
+
+size_t mla_workspace(int32_t batch, int32_t q_heads, int32_t max_len) {
+    int chunk = 0, nc = 0;
+    mla_plan(batch, q_heads, max_len, &chunk, &nc);
+    return mla_partials(batch, q_heads, nc);
+}
+
+// The largest mla_workspace of any max_len up to this one: the chunks' size
+// grows in steps, and the number of chunks falls at each.
+size_t mla_workspace_bound(int32_t batch, int32_t q_heads, int32_t max_len) {
+    const int64_t sms = sm_count();
+    int64_t most = 1;
+    if (mla_use_tc(q_heads)) {
+        // for every chunk size, the longest max_len that is cut into chunks no
+        // larger: batch * max_len / (4 sms) <= c (4096: any)
+        for (int64_t c = 256; c <= 4096; c += rc_mla_tc::TN) {
+            int64_t len = max_len;
+            if (c < 4096 && batch > 0) {
+                const int64_t last = ((c + 1) * 4 * sms - 1) / batch;
+                len = last < len ? last : len;
+            }
+            const int64_t nc = (len + c - 1) / c;
+            most = nc > most ? nc : most;
+        }
+    } else {
+        const int64_t base = (int64_t)batch * (q_heads / rc_mla::HB);
+        const int64_t splits = base > 0 ? (4 * sms + base - 1) / base : 1;
+        const int64_t max_splits = max_len > 0 ? ((int64_t)max_len + 1023) / 1024 : 1;
+        most = splits < max_splits ? splits : max_splits;
+    }
+    return mla_partials(batch, q_heads, most);
 }
 
 rc_status mla_decode(const rc_attn_desc* desc, const void* q, const rc_kv_table* kv, int32_t batch, void* out,

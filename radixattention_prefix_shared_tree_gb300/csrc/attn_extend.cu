@@ -49,6 +49,7 @@ constexpr int kSplitKeys = 512;
 struct ExtendPlan {
     int chunk = 0, n_chunks = 1;
     size_t part_o = 0, total = 0;
+    size_t bound = 0;  // the largest total of any max_len up to this one
 };
 
 ExtendPlan plan_extend(const rc_attn_desc* d, int32_t batch, int32_t max_q, int32_t max_len) {
@@ -69,8 +70,11 @@ ExtendPlan plan_extend(const rc_attn_desc* d, int32_t batch, int32_t max_q, int3
     pl.n_chunks = (max_len + pl.chunk - 1) / pl.chunk;
     if (pl.n_chunks < 2) return ExtendPlan();
     const size_t rows = (size_t)max_rows * d->q_heads * pl.n_chunks;
-    pl.part_o = (rows * P.head_dim_v * sizeof(float) + 255) & ~size_t(255);
-    pl.total = pl.part_o + ((rows * sizeof(float) + 255) & ~size_t(255));
+    auto bytes = [&](size_t n) { return (n * sizeof(float) + 255) & ~size_t(255); };
+    pl.part_o = bytes(rows * P.head_dim_v);
+    pl.total = pl.part_o + bytes(rows);
+    const size_t most_rows = (size_t)max_rows * d->q_heads * splits;  // n_chunks, rounded, can fall as max_len grows
+    pl.bound = bytes(most_rows * P.head_dim_v) + bytes(most_rows);
     return pl;
 }
 
@@ -79,7 +83,7 @@ ExtendPlan plan_extend(const rc_attn_desc* d, int32_t batch, int32_t max_q, int3
 extern "C" rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t max_q,
                                            int32_t max_len, size_t* bytes) {
     if (!desc || !bytes || batch < 0 || max_q < 0 || max_len < 0) return RC_ERR_ARG;
-    *bytes = plan_extend(desc, batch, max_q, max_len).total;
+    *bytes = plan_extend(desc, batch, max_q, max_len).bound;
     return RC_OK;
 }
 

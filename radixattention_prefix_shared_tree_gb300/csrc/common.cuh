@@ -277,6 +277,7 @@ rc_status store_fp4(const rc_pool_desc* pool, const int32_t* slots, const void* 
                     int32_t* table, const int32_t* table_pos, cudaStream_t st);
 // latent (MLA) decode, attn_decode_mla.cu
 size_t mla_workspace(int32_t batch, int32_t q_heads, int32_t max_len);
+size_t mla_workspace_bound(int32_t batch, int32_t q_heads, int32_t max_len);
 rc_status mla_decode(const rc_attn_desc* desc, const void* q, const rc_kv_table* kv, int32_t batch, void* out,
                      float* lse, void* ws, size_t ws_bytes, cudaStream_t st);
 inline rc_status launch_status(cudaError_t e) { return e == cudaSuccess ? RC_OK : RC_ERR_CUDA; }

@@ -519,7 +519,7 @@ class DeviceEngine:
         casc = lay.casc if lay.use_cascade else None
         lay.kv_tables = None
         dec_max = lay.dec_max.tolist() if T else []
-        # the workspace attn_decode plans grows with max_len: size it for the largest
+        # attn_decode's workspace for the largest max_len serves every smaller one
         lay.ws_bytes = self._decode_ws(B, [max(dec_max)] if dec_max else [], casc)
         lay.ws = self.workspace(lay.ws_bytes)
         lay.ws_ptr = lay.ws.data_ptr()
