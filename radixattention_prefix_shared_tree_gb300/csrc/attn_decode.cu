@@ -368,6 +368,8 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
     if (use_casc && (!casc->seg_slots || !casc->seg_indptr || !casc->seg_row_indptr || !casc->seg_rows ||
                      !casc->req_seg_indptr || !casc->req_seg_pos))
         return RC_ERR_ARG;
+    // the cascade masks scores and takes their largest before it scales them
+    if (use_casc && !(desc->sm_scale > 0.f)) return RC_ERR_ARG;
     const rc_pool_desc& P = desc->pool;
     const int D = P.head_dim_k;
     if (P.mla || P.head_dim_v != D || !P.v) return RC_ERR_UNSUPPORTED;
@@ -383,9 +385,7 @@ rc_status decode_impl(const rc_attn_desc* desc, const void* q, const void* k_new
         s = rc_host::check_fp4(P);
         if (s != RC_OK) return s;
         if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;
-        // the cascade takes the largest score for the largest scaled one; the
-        // table pass turns a negative scale into Q
-        if (use_casc ? !(desc->sm_scale > 0.f) : desc->sm_scale != desc->sm_scale) return RC_ERR_ARG;
+        if (desc->sm_scale != desc->sm_scale) return RC_ERR_ARG;  // (a negative one is turned into Q)
     }
     const int G = desc->q_heads / P.kv_heads;
     unsigned char* w = static_cast<unsigned char*>(ws);

@@ -104,8 +104,8 @@ extern "C" rc_status attn_extend(const rc_attn_desc* desc, const void* q, const 
         const rc_status s = rc_host::check_fp4(P);
         if (s != RC_OK) return s;
         if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return RC_ERR_ARG;
-        if (!(desc->sm_scale > 0.f)) return RC_ERR_ARG;  // the largest score has to be the largest scaled one
     }
+    if (!(desc->sm_scale > 0.f)) return RC_ERR_ARG;  // scores are masked, and their largest taken, before they are scaled
     rc::MQParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.pool_k = static_cast<const __nv_bfloat16*>(P.k);
