@@ -33,8 +33,8 @@ from dataclasses import dataclass, field
 import numpy as np
 
 from . import (RC_COMMIT_FINISH, RC_COMMIT_PREFILL, RC_ERR_NOMEM, RC_FCFS, RC_LPM, RC_OK, RCError, attn_decode,
-               attn_decode_workspace, attn_extend, kv_store, lib, make_attn_desc, make_cascade, make_kv_table,
-               make_pool_desc, rc_decode_step, rc_request)
+               attn_decode_workspace, attn_extend, attn_extend_workspace, kv_store, lib, make_attn_desc, make_cascade,
+               make_kv_table, make_pool_desc, rc_decode_step, rc_request)
 
 
 @dataclass
@@ -509,9 +509,12 @@ class DeviceEngine:
             self._call("kv_store", 1, ("store", n), lambda: kv_store(self.pool, slots_dev, k, v))
 
     def extend(self, lay, q, out, lse=None):
-        kv = lay.extend_table
-        self._call("attn_extend", 1, ("extend", lay),
-                   lambda: attn_extend(self.desc, q, lay.qo_indptr, kv, lay.batch_size, lay.max_q, out, lse))
+        kv, ws = lay.extend_table, None
+        if self.kv_fp4:   # few tokens over long prefixes: the keys split over more CTAs, then a merge
+            nbytes = attn_extend_workspace(self.desc, lay.batch_size, lay.max_q, kv.max_len)
+            ws = self.workspace(nbytes) if nbytes else None
+        self._call("attn_extend", 1 if ws is None else 2, ("extend", lay),
+                   lambda: attn_extend(self.desc, q, lay.qo_indptr, kv, lay.batch_size, lay.max_q, out, lse, ws))
 
     # ---- decode loop: per-step arguments built once per batch, two C calls per step
     def prepare_decode(self, lay):
