@@ -358,7 +358,8 @@ typedef struct rc_kv_table {
  * scale = amax|x| / 448 (fp32, rounded to nearest) and codes
  * e4m3(x_i / scale) (fp32 quotient rounded to nearest, then to the nearest
  * E4M3 value, ties to even, saturating at +-448); an all-zero row stores scale
- * 0 and zero codes.
+ * 0 and zero codes.  A NaN stores the NaN code (the amax passes over it); a row
+ * with an infinity reads as NaN.
  * 4-bit pool: per block of 16, scale = amax|x| / 6 (fp32, rounded to nearest)
  * rounded to the scale's 5 + 3 bits (nearest, ties to even, steps of 2^-17
  * below 2^-14, at most 10240), and codes e2m1(x_i / scale) (fp32 quotient

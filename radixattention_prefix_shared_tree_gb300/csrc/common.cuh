@@ -154,6 +154,10 @@ RC_DEV uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Eight bits of an E4M3 code for a row whose scale is 0: zeros (of any sign) as
+// 0, a NaN as itself, which a scale of 0 keeps.
+RC_DEV uint32_t e4m3_nan_or_zero(float x) { return x != x ? 0x7fu : 0u; }
+
 // Two E4M3 codes (low byte first) to two f16 (low half first); exact, since
 // every E4M3 value is an f16 value.
 RC_DEV uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
