@@ -34,20 +34,24 @@ P = C.POINTER
 
 
 class rc_pool_desc(C.Structure):
+    _dev = None     # CUDA device of the arrays (make_pool_desc; None: not known, e.g. filled by hand)
     _fields_ = [("k", VP), ("v", VP), ("n_slots", I64), ("kv_heads", I32), ("head_dim_k", I32),
                 ("head_dim_v", I32), ("mla", I32), ("err", VP), ("kv_fp8", I32), ("k_scale", VP),
                 ("v_scale", VP), ("k_bscale", VP), ("v_bscale", VP)]
 
 
 class rc_rope_desc(C.Structure):
+    _dev = None
     _fields_ = [("cos_sin", VP), ("max_pos", I32), ("rot_dim", I32), ("offset", I32), ("interleaved", I32)]
 
 
 class rc_attn_desc(C.Structure):
+    _dev = None
     _fields_ = [("pool", rc_pool_desc), ("q_heads", I32), ("sm_scale", C.c_float)]
 
 
 class rc_kv_table(C.Structure):
+    _dev = None
     _fields_ = [("slots", VP), ("start", VP), ("len", VP), ("max_len", I32), ("table_len", I64)]
 
 
@@ -446,13 +450,24 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _on_device(call, *tensors):
-    """The kernels run on the current device and read these tensors there."""
+def _on_device(call, devs, *tensors):
+    """The kernels run on the current device and read these descriptors' arrays
+    (their devices) and tensors there."""
     import torch
     dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{call}: a tensor is on {t.device}, the current device is cuda:{dev}")
+    for d in devs:
+        if d != dev and d is not None:
+            raise ValueError(f"{call}: a descriptor's arrays are on device {d} (-1: the host, -2: several), the current "
+                             f"device is {dev}")
+
+
+def _device_of(*tensors) -> int:
+    """Device index of the tensors (None among them): -1 the host, -2 several."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    return devs.pop() if len(devs) == 1 else -2
 
 
 def make_pool_desc(k, v, err=None, mla: bool = False, head_dim_v: int | None = None, k_scale=None,
@@ -495,6 +510,7 @@ def make_pool_desc(k, v, err=None, mla: bool = False, head_dim_v: int | None = N
         d.head_dim_k, d.head_dim_v = 2 * k.shape[2], 2 * v.shape[2]
         d.k_bscale, d.v_bscale = k_bscale.data_ptr(), v_bscale.data_ptr()
     d._keep = (k, v, err, k_scale, v_scale, k_bscale, v_bscale)   # raw pointers inside: keep the tensors alive with it
+    d._dev = _device_of(k, v, k_scale, v_scale, k_bscale, v_bscale)
     return d
 
 
@@ -504,6 +520,7 @@ def make_attn_desc(pool: rc_pool_desc, q_heads: int, sm_scale: float) -> rc_attn
     a.q_heads = int(q_heads)
     a.sm_scale = float(sm_scale)
     a._keep = getattr(pool, "_keep", None)
+    a._dev = pool._dev
     return a
 
 
@@ -513,6 +530,8 @@ def make_kv_table(slots, start, length, max_len: int, table_len: int | None = No
     t.max_len = int(max_len)
     t.table_len = int(slots.numel() if table_len is None else table_len)
     t._keep = (slots, start, length)   # raw pointers inside: keep the tensors alive with it
+    dev = slots.get_device()
+    t._dev = dev if start.get_device() == dev and length.get_device() == dev else -2
     return t
 
 
@@ -567,6 +586,7 @@ def make_rope_desc(cos_sin, interleaved: bool = False, offset: int = 0) -> rc_ro
     r.max_pos, r.rot_dim = cos_sin.shape
     r.offset, r.interleaved = int(offset), int(bool(interleaved))
     r._keep = (cos_sin,)
+    r._dev = cos_sin.get_device()
     return r
 
 
@@ -601,7 +621,7 @@ def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_ne
     rows dense, tokens any distance apart; v_new None for a latent pool; q_out
     None rotates q in place.  slots, positions, table_pos: int32 [n]."""
     st = (_host_call or _host_store_rope())(C.addressof(pool), C.addressof(rope), slots, positions, k_new, v_new, q, q_out,
-                                            table, table_pos, stream)
+                                            table, table_pos, stream, pool._dev, rope._dev)
     if st:
         _check("kv_store_rope", st)
 
@@ -686,7 +706,7 @@ def attn_cross_workspace(desc: rc_attn_desc, batch: int, max_q: int, max_len: in
 def attn_cross(desc: rc_attn_desc, q, qo_indptr, kv: rc_kv_table, batch: int, max_q: int, out, lse=None,
                ws=None, stream=None):
     """Every token of row b over all the keys of the row (see the header)."""
-    _on_device("attn_cross", q, qo_indptr, out, lse, ws)
+    _on_device("attn_cross", (desc._dev, kv._dev), q, qo_indptr, out, lse, ws)
     st = lib().attn_cross(C.byref(desc), _ptr(q), _ptr(qo_indptr), C.byref(kv), batch, max_q, _ptr(out), _ptr(lse),
                           _ptr(ws), _bytes(ws), _stream(stream))
     _check("attn_cross", st)

@@ -128,12 +128,13 @@ static long long ids(PyObject* t, const char* name, long long n) {
     return sh[0];
 }
 
-/* kv_store_rope(pool, rope, slots, positions, k_new, v_new, q, q_out, table, table_pos, stream) -> status.
- * pool, rope: addresses of the descriptors; stream: None for the current one. */
+/* kv_store_rope(pool, rope, slots, positions, k_new, v_new, q, q_out, table, table_pos, stream, pool's device,
+ * rope's device) -> status.  pool, rope: addresses of the descriptors; stream: None for the current one; devices:
+ * None where they are not known. */
 static PyObject* store_rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     (void)self;
-    if (na != 11 || !fn_store_rope) {
-        PyErr_SetString(PyExc_TypeError, "kv_store_rope: bind() first, then 11 arguments");
+    if (na != 13 || !fn_store_rope) {
+        PyErr_SetString(PyExc_TypeError, "kv_store_rope: bind() first, then 13 arguments");
         return NULL;
     }
     const rc_pool_desc* pool = (const rc_pool_desc*)(uintptr_t)PyLong_AsUnsignedLongLong(a[0]);
@@ -173,6 +174,17 @@ static PyObject* store_rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     static const char* const names[8] = {"slots", "positions", "k_new", "v_new", "q", "q_out", "table", "table_pos"};
     for (int i = 0; i < 8; ++i)
         if (t[i] != Py_None && address(t[i], names[i], dev, &p[i])) return NULL;
+    for (int i = 11; i < 13; ++i) {
+        if (a[i] == Py_None) continue;
+        const long long d_dev = PyLong_AsLongLong(a[i]);
+        if (PyErr_Occurred()) return NULL;
+        if (d_dev != dev) {
+            PyErr_Format(PyExc_ValueError,
+                         "kv_store_rope: the %s on device %lld (-1: the host, -2: several), the current device is %lld",
+                         i == 11 ? "pool's arrays are" : "rotation table is", d_dev, dev);
+            return NULL;
+        }
+    }
     unsigned long long stream;
     PyObject* s = a[10] != Py_None ? PyObject_GetAttr(a[10], s_cuda_stream) : NULL;
     if (a[10] == Py_None) {
