@@ -352,7 +352,9 @@ typedef struct rc_kv_table {
  * KV of its tokens].  k_new: [n][kv_heads][head_dim_k] bf16; v_new:
  * [n][kv_heads][head_dim_v] (NULL for the latent layout).  Row i goes to slot
  * slots[i].  If table and table_pos are both non-NULL, also
- * table[table_pos[i]] = slots[i] (appends to the slot tables).
+ * table[table_pos[i]] = slots[i] (appends to the slot tables; the caller sees to
+ * it that table_pos lies inside the table).  Slots of one call are distinct: of
+ * two tokens for one slot, parts of either may stay.
  * A slot outside [0, n_slots) is skipped and flags RC_ERR_DEVICE in pool->err.
  * FP8 pool: each (token, head) row x of head_dim bf16 values is stored as
  * scale = amax|x| / 448 (fp32, rounded to nearest) and codes
@@ -396,7 +398,8 @@ typedef struct rc_rope_desc {
  * of 8, so slices of one projection's output can be passed; 16-byte aligned).
  * q_out: the rotated queries (bf16), rows q_out_stride apart (at least
  * q_heads * head_dim); it may be q itself with the same stride, and then only
- * the rotated columns are written, and must not overlap q otherwise.  q and
+ * the rotated columns are written, and must overlap neither q otherwise nor
+ * k_new or v_new.  q and
  * q_out NULL: K and V only.  v_new is NULL for the latent layout, whose rows
  * (one of 576 columns) rotate like the others.  slots, table, table_pos as in
  * kv_store.  A token whose slot is outside [0, n_slots) stores no K and V (its
@@ -565,7 +568,9 @@ rc_status attn_extend_workspace(const rc_attn_desc* desc, int32_t batch, int32_t
  * 0..p causally.  q and out: [sum n_b][q_heads][head_dim] bf16.
  * max_q: host bound on n_b.  lse: NULL or [sum n_b][q_heads] fp32.
  * An infinity or a NaN in a new token's V may make the row's earlier new tokens
- * NaN too (a weight of zero times it).
+ * NaN too (a weight of zero times it).  A row outside the table, or (with the
+ * workspace, where it is used) longer than kv->max_len, flags RC_ERR_DEVICE; its
+ * output is not written, or zeros where the workspace is used.
  * ws: NULL, or attn_extend_workspace bytes, 256-byte aligned; calls that can
  * overlap on the GPU need a workspace each.
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED, RC_ERR_CUDA. */
@@ -586,7 +591,10 @@ rc_status attn_cross_workspace(const rc_attn_desc* desc, int32_t batch, int32_t 
  * n_b = qo_indptr[b+1]-qo_indptr[b] tokens (0 <= n_b <= max_q) and len[b] keys
  * (0 <= len[b] <= kv->max_len); a row without keys gives zeros and an lse of
  * -infinity.  q and out: [sum n_b][q_heads][head_dim] bf16, 16-byte aligned;
- * rows of out behind the last token are not written.  lse: NULL or
+ * rows of out behind the last token are not written.  Up to eight (token, query
+ * head) pairs per KV head take the decode kernels, more the one of attn_extend;
+ * the softmax weights are rounded to bf16 over a bf16 pool, to f16 over the
+ * others, as in attn_decode and attn_extend.  lse: NULL or
  * [sum n_b][q_heads] fp32, natural log.  bf16, FP8 (head_dim 128) and 4-bit
  * pools, head_dim 64 or 128, 1, 2, 4 or 8 query heads per KV head; sm_scale > 0.
  * ws: attn_cross_workspace bytes, 256-byte aligned (NULL when that is 0); calls
@@ -595,7 +603,8 @@ rc_status attn_cross_workspace(const rc_attn_desc* desc, int32_t batch, int32_t 
  * computed, a row of keys outside the table or longer than max_len is taken as
  * empty; both flag RC_ERR_DEVICE in the pool's err, as a slot outside the pool
  * does (its key then reads as zeros).
- * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED, RC_ERR_CUDA. */
+ * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED (head layout; more than 65,535 rows, or
+ * parts of rows, of more than eight pairs), RC_ERR_CUDA. */
 rc_status attn_cross(const rc_attn_desc* desc, const void* q, const int32_t* qo_indptr,
                      const rc_kv_table* kv, int32_t batch, int32_t max_q, void* out, float* lse,
                      void* ws, size_t ws_bytes, rc_stream_t stream);

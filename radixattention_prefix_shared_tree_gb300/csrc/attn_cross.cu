@@ -8,11 +8,11 @@
 // that share a K/V head, max_q * q_heads / kv_heads:
 //  * at most 8: bound by the K/V read once; the decode table pass, one warp
 //    per (row, KV head, key chunk) with the pairs as its columns (32 rows of
-//    1500 bf16 keys, 16 KV heads of 64: 35.8 us, 5.5 TB/s);
+//    1500 bf16 keys, 16 KV heads of 64: 38.2 us a call, 5.15 TB/s);
 //  * more: the tcgen05 kernel of attn_extend without the causal edge, 256
 //    pairs per CTA, bound by the hand-offs of its tiles (6 rows of 900-1024
-//    tokens over 4095 4-bit keys, 32 heads over 8 of 128: 323 us, 1180 TFLOP/s);
-//    where its grid would leave SMs idle the keys are split over CTAs.
+//    tokens over 4095 4-bit keys, 32 heads over 8 of 128: 328 us a call, 1160
+//    TFLOP/s); where its grid would leave SMs idle the keys are split over CTAs.
 // Split keys leave normalised partials that a merge joins (attn_split_merge.cuh,
 // or for the 4-bit table pass merge_runs_kernel).
 
@@ -25,7 +25,11 @@ namespace {
 
 using namespace rc_dec;
 
-constexpr int kFewColumns = 8;   // the n = 8 side of the table pass's products
+// The n = 8 side of the table pass's products.  At 8 pairs, 8 KV heads of 128 and
+// 1500 keys a call takes, in the table pass and in the many-row kernel: 32 rows
+// 42 and 69 us (bf16), 32 and 80 (E4M3), 40 and 54 (4 bits); 8 rows 22 and 24, 19
+// and 27, 21 and 21; one row 17 and 14, 15 and 15, 13 and 13.
+constexpr int kFewColumns = 8;
 
 struct CrossPlan {
     bool few = false, runs = false;  // runs: the 4-bit table pass over equal runs of keys

@@ -9,8 +9,9 @@
 // four neighbouring heads' together where there are that many (COOP).  A key's
 // row is 72 bytes at D = 128 (64 of codes, 8 of scales) against 256 in bf16, so
 // HBM gives a tile fewer cycles than its instructions take: at 256 rows of
-// 512-5119 keys, 8 KV heads, the pass takes 166 us, its loads alone 131 and its
-// arithmetic alone 132; 123 would be HBM's copy rate.  What that decides:
+// 512-5119 keys, 8 KV heads, the pass takes 160 us and the merge behind it 6, the
+// pass's loads alone 131 and its arithmetic alone 132; 123 would be HBM's copy
+// rate.  What that decides:
 //  * code times scale is exactly an f16 value, so both products run on f16
 //    mma.sync with the values themselves and the softmax sees no scales;
 //  * the order of the head's dims inside the products is free as long as both
@@ -21,8 +22,9 @@
 //    interleaved before they are widened (half a logic instruction per pair
 //    instead of a byte permute each);
 //  * 32 keys per tile share one round of max shuffles and one rescale test.
-// Measured and left out at that size: a third stage 169 us, eight warps a CTA
-// 179, five or six CTAs per SM 211 and 251 (registers spill).
+// Measured and left out at that size (against 166 us with the merge): a third
+// stage 169, eight warps a CTA 179, five or six CTAs per SM 211 and 251
+// (registers spill).
 #pragma once
 
 #include "attn_decode.cuh"
@@ -104,7 +106,9 @@ constexpr int kMergeWarps = 8;
 // Apart, every warp reads 64 and 8 bytes of them, and the number of requests,
 // not their bytes, bounds the loads: at 256 rows of 512-5119 keys the loads
 // alone took 152 us against 123 without the scales' eight-byte reads.  Other
-// head counts keep a ring per warp.
+// head counts keep a ring per warp.  A call over those rows: 8 KV heads 169 us
+// together, 315 apart, 4 heads 94 and 124; 3 heads, apart, 99 us, 2 heads 56, one
+// head 45 (floors 46, 31 and 15).
 template <int D, int NC, bool FUSED, bool CROSS, bool COOP>
 __global__ void __launch_bounds__(32 * fp4::kWarps, fp4::kCtasPerSm) decode_fp4_kernel(const DecParams p, int n_items) {
     using namespace fp4;

@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
                 rc::mma_f16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
             }
         } else {
+            // P to bf16, V's type (one product takes one type); the denominator
+            // keeps the fp32 terms
             const uint32_t pb0 = rc::movmatrix_trans(rc::pack_bf16(p0, p1));
             const uint32_t pb1 = rc::movmatrix_trans(rc::pack_bf16(p2, p3));
             const int key = (lane & 7) + (lane >> 4) * 8;

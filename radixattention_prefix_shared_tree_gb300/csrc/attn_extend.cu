@@ -41,8 +41,9 @@ cudaError_t dispatch(int G, const rc::MQParams& p, int batch, int max_q, int kv_
     }
 }
 
-// Over a 4-bit pool, a grid that would leave most SMs idle splits the keys, at
-// least four tiles a CTA, where there are enough of them to pay for the
+// Over a 4-bit pool (the other formats' calls never ask for a workspace and stay
+// whole), a grid that would leave most SMs idle splits the keys, at least four
+// tiles a CTA, where there are enough of them to pay for the
 // merge (1 row of 8 tokens over 4,000 keys: 57 us whole, 12 split; 4 rows of 40
 // over 340: 12.3 whole, 14.1 split; over 1,040: 22.4 and 16.3).
 constexpr int kSplitKeys = 512;

@@ -670,6 +670,8 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) attn_tc2_kernel(const rc::M
                     const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), sc, nmu);
                     const float2 e = make_float2(ex2(x.x), ex2(x.y));
                     ls[i & 3] = fadd2(ls[i & 3], e);
+                    // P to the type of V's operand (one product takes one type): bf16
+                    // keeps 8 bits of a weight, f16 11; the sum keeps the fp32 terms
                     if constexpr (FP8) pk[i] = rc::pack_f16(e.x * tsc[TN + 2 * i], e.y * tsc[TN + 2 * i + 1]);
                     else if constexpr (FP4) pk[i] = rc::pack_f16(e.x, e.y);
                     else pk[i] = rc::pack_bf16(e.x, e.y);
