@@ -258,8 +258,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
                 grow = true;
             }
         }
-        const float mu0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) + (FP8 ? unit_f : 0.f);
-        const float mu1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) + (FP8 ? unit_f : 0.f);
+        float mu0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
+        float mu1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        if constexpr (FP8) mu0 += unit_f, mu1 += unit_f;
         float p0 = rc::fast_exp2(s[0] - mu0), p1 = rc::fast_exp2(s[1] - mu1);
         float p2 = rc::fast_exp2(s[2] - mu0), p3 = rc::fast_exp2(s[3] - mu1);
         if (__any_sync(0xffffffffu, grow)) {
@@ -352,9 +353,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
         sE[(2 * t_lane + 1) * D + d1] = o[mt][3] * inv1;
     }
     if (g_lane == 0) {
-        const float back = FP8 ? unit_f : 0.f;
-        sOwn[2 * t_lane] = rc::log2_sum(m_run[0] + back, l_run[0]);
-        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1] + back, l_run[1]);
+        if constexpr (FP8) m_run[0] += unit_f, m_run[1] += unit_f;
+        sOwn[2 * t_lane] = rc::log2_sum(m_run[0], l_run[0]);
+        sOwn[2 * t_lane + 1] = rc::log2_sum(m_run[1], l_run[1]);
     }
     __syncwarp();
     decode_epilogue<D, G, FUSED, CROSS>(p, w, sE, sOwn, seg, first_row, lane);

@@ -223,7 +223,7 @@ RC_DEV float fast_exp2(float x) { return exp2f(x); }
 // A softmax part's log-sum-exp in log2 units from its reference m and sum l.
 // None: -infinity, no weight.  A NaN sum (a key of the part is NaN): +infinity,
 // so that a merge turns the row into NaN instead of leaving the part out.
-RC_DEV float log2_sum(float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; }
+RC_DEV float log2_sum(float m, float l) { return l == l ? m + log2f(l) : INFINITY; }
 
 // 2^e for -126 <= e <= 127.
 RC_DEV float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
