@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta, kCtasPerSm) decode_split_ke
                 grow = true;
             }
         }
-        float mu0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        float mu1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
-        if constexpr (FP8) mu0 += unit_f, mu1 += unit_f;
+        // (-0: the one zero whose addition is no instruction)
+        const float mu0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) + (FP8 ? unit_f : -0.f);
+        const float mu1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) + (FP8 ? unit_f : -0.f);
         float p0 = rc::fast_exp2(s[0] - mu0), p1 = rc::fast_exp2(s[1] - mu1);
         float p2 = rc::fast_exp2(s[2] - mu0), p3 = rc::fast_exp2(s[3] - mu1);
         if (__any_sync(0xffffffffu, grow)) {
