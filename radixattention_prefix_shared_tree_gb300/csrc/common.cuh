@@ -154,9 +154,9 @@ RC_DEV uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Eight bits of an E4M3 code for a row whose scale is 0: zeros (of any sign) as
-// 0, a NaN as itself, which a scale of 0 keeps.
-RC_DEV uint32_t e4m3_nan_or_zero(float x) { return x != x ? 0x7fu : 0u; }
+// Four E4M3 codes of zeros (of any sign) and NaNs with the zeros as 0: a NaN's
+// code is 0x7f, the only one here with its lowest bit set.
+RC_DEV uint32_t e4m3_only_nans(uint32_t codes) { return codes & ((codes & 0x01010101u) * 0x7fu); }
 
 // Two E4M3 codes (low byte first) to two f16 (low half first); exact, since
 // every E4M3 value is an f16 value.

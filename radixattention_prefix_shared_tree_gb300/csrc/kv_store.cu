@@ -80,13 +80,16 @@ __global__ void __launch_bounds__(256) kv_store_fp8_kernel(const int32_t* __rest
             const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
                 make_float2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)), __NV_SATFINITE, __NV_E4M3);
             codes = (uint32_t)lo | ((uint32_t)hi << 16);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) codes |= rc::e4m3_nan_or_zero(x[k]) << (8 * k);
         }
         const int64_t row = (int64_t)s * heads + h;
         reinterpret_cast<uint32_t*>((is_v ? pool_v : pool_k) + row * D)[lane] = codes;
         if (lane == 0) (is_v ? v_scale : k_scale)[row] = scale;
+        if (!(scale > 0.f)) {  // a row of zeros and NaNs: the NaNs, as a second store (in the first's select: 10 % more)
+            uint32_t nans = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nans |= (x[k] != x[k] ? 0x7fu : 0u) << (8 * k);
+            if (nans) reinterpret_cast<uint32_t*>((is_v ? pool_v : pool_k) + row * D)[lane] = nans;
+        }
         if (lane == 0 && j == 0 && table) table[__ldg(table_pos + t)] = s;
     }
 }

@@ -97,17 +97,15 @@ RC_DEV uint32_t e2m1_codes(const float (&x)[8], uint32_t byte) {
 }
 // Eight E4M3 codes of x / scale, x[0] in the low byte.
 RC_DEV uint2 e4m3_codes(const float (&x)[8], float scale) {
+    const bool some = scale > 0.f;  // otherwise a row of zeros and NaNs: as it is
+    const float by = some ? scale : 1.f;
     uint32_t w[4];
-    if (!(scale > 0.f)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = rc::e4m3_nan_or_zero(x[2 * i]) | (rc::e4m3_nan_or_zero(x[2 * i + 1]) << 8);
-        return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale)),
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], by), __fdiv_rn(x[2 * i + 1], by)),
                                         __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    const uint2 c = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    return some ? c : make_uint2(rc::e4m3_only_nans(c.x), rc::e4m3_only_nans(c.y));
 }
 
 // U: units per head row (D / 16).  ROT 0: no rotation; 1: pairs half the
