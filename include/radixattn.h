@@ -481,7 +481,8 @@ rc_status attn_decode(const rc_attn_desc* desc, const void* q, const rc_kv_table
  * row's table part, not in a cascade segment (cascade segments hold cached
  * keys only).  A bad slot id for it is skipped and flags RC_ERR_DEVICE.
  * Same workspace (attn_decode_workspace) and errors as attn_decode; the latent
- * layout returns RC_ERR_UNSUPPORTED (use kv_store + attn_decode). */
+ * layout and pools of codes return RC_ERR_UNSUPPORTED (use kv_store +
+ * attn_decode). */
 rc_status attn_decode_append(const rc_attn_desc* desc, const void* q, const void* k_new,
                              const void* v_new, const rc_kv_table* kv, int32_t batch,
                              const rc_cascade* cascade, void* out, float* lse, void* ws,
@@ -491,7 +492,7 @@ rc_status attn_decode_append(const rc_attn_desc* desc, const void* q, const void
  * step's row lengths (device) and their host bound, replacing kv->len and
  * kv->max_len.  store_slots: NULL, or [batch] device slot ids that kv_store
  * fills from k_new/v_new before the step's attention (the latent layout, the
- * FP8 pool).  With store_slots NULL and k_new set the step is an
+ * FP8 and 4-bit pools).  With store_slots NULL and k_new set the step is an
  * attn_decode_append; with both NULL a plain attn_decode.  ev_begin/ev_end:
  * NULL or a cudaEvent_t recorded on the stream before the step's first launch
  * and after its last (per-step timing). */
