@@ -380,10 +380,6 @@ def _plan(s):
                                       v_bscale=s.get("v_bscale"))
     if case["op"] == "append":
         p["rope"] = ra.make_rope_desc(s["table"], interleaved=case["inter"], pair_axis=_pair_axis(case))
-        if "k_bscale" in s:
-            p["all"] = torch.arange(s["k"].shape[0], dtype=torch.int32, device=s["k"].device)
-            p["k"], p["v"] = (torch.empty(*s[n].shape[:-1], 2 * s[n].shape[-1], dtype=torch.bfloat16, device=s[n].device)
-                              for n in ("k", "v"))
     return p
 
 
@@ -396,8 +392,6 @@ def _run_own(s):
         ra.attn_prompt(s["q"], s["k"], s["v"], s["indptr"], s["scale"], s["out"], s["lse"], err=s["err"])
     elif op == "append":
         ra.kv_store_rope(p["pool"], p["rope"], s["slots"], s["positions"], s["k_new"], s["v_new"], s["q"], s["q_out"])
-        if "all" in p:      # the pool's values, as a user reads them
-            ra.kv_load(p["pool"], p["all"], p["k"], p["v"])
     elif op == "load":
         ra.kv_load(p["pool"], s["slots"], s["k_out"], s["v_out"])
     else:
@@ -422,9 +416,7 @@ def run(state):
     if op == "append":
         out = [s["q_out"]]
         for name in ("k", "v"):
-            if own and "k_bscale" in s:
-                out.append(s["plan"][name])
-            elif "k_bscale" in s:
+            if "k_bscale" in s:
                 out.append(_from_blocks(s[name], s[name + "_bscale"]).bfloat16())     # (at most six significant bits: exact)
             else:
                 out += [s[name]] + ([s[name + "_scale"]] if "k_scale" in s else [])
