@@ -16,6 +16,8 @@
 
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace {
 
 constexpr int kWarps = 4;  // per block
@@ -348,42 +350,74 @@ __global__ void __launch_bounds__(32 * kWarps) store_rope_kernel(const StorePara
     }
 }
 
+// Warps of the kernel that the GPU holds at once (the occupancy does not depend on the call).
+template <int U, int FMT, int ROT, int UN, bool AXES>
+int64_t resident() {
+    static const int an_sm = [] {
+        int blocks = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, store_rope_kernel<U, FMT, ROT, UN, AXES>, 32 * kWarps, 0) !=
+            cudaSuccess)
+            blocks = 0;
+        return blocks > 0 ? blocks * kWarps : 16;
+    }();
+    return (int64_t)an_sm * rc_host::sm_count();
+}
+
 template <int U, int FMT, int ROT, bool AXES = false>
 rc_status launch(StoreParams& p, cudaStream_t st) {
     const int units = (p.kv_heads * (p.v ? 2 : 1) + (p.q ? p.q_heads : 0)) * U;
     // A warp takes one 32-unit pass of its token while that keeps the grid within a few
-    // waves.  Beyond, it takes several, which share the token's positions and angles,
-    // kAhead of them with their loads on the way together: half of kPasses while all
-    // warps are resident at once, else kPasses, as a token's first loads (slot, position,
-    // angles, values, one after the other) then cost more than a wave half empty.  8 KV
-    // and 32 query heads of 128, 6 against 12 passes a warp: 1,200 tokens into an 8-bit
-    // pool 12.6 and 15.2 us, 1,600 19.5 and 16.1, 9,001 58.5 and 48.3; a bf16 pool,
-    // 9,001 tokens, 42.1 and 40.6.  Loads of 6 passes ahead instead of 3 (120 registers
-    // a thread, 16 warps an SM): 66.3 us into the 8-bit pool, 46.4 into bf16.
-    // Latent rows keep 4 and 4 (1,023 tokens of 128 query heads: 56 us, 60 with 2 ahead), but
-    // with several axes a unit's angles take registers too: 9,001 tokens of 16, 130 and 86.
-    constexpr int kPasses = U == 36 ? 4 : 12, kAhead = U != 36 ? 3 : AXES ? 2 : 4;
+    // waves.  Beyond, it takes several, which share the token's positions and angles, with
+    // the loads of some of them on their way together.
     const int passes = (units + 31) / 32;
-    const bool many = (int64_t)p.n * passes > (int64_t)rc_host::sm_count() * 64;
-    auto* const kernel = store_rope_kernel<U, FMT, ROT, kAhead, AXES>;
-    auto warps_of = [&](int most) { return (passes + most - 1) / most; };  // per token, of as many passes each as any other
-    int cut = passes;
-    if (many) {
-        static const int resident = [&] {  // warps an SM
-            int blocks = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, 32 * kWarps, 0) != cudaSuccess) blocks = 0;
-            return blocks * kWarps;
-        }();
-        cut = warps_of(kPasses / 2);
-        if (U == 36 || (int64_t)p.n * cut > (int64_t)rc_host::sm_count() * resident) cut = warps_of(kPasses);
+    int cut = passes, ahead = 1;  // warps a token, of as many passes each as any other; passes ahead
+    if (passes > 1 && (int64_t)p.n * passes > (int64_t)rc_host::sm_count() * 64) {
+        auto warps_of = [&](int most) { return (passes + most - 1) / most; };
+        if constexpr (U == 36) {
+            // Latent rows: 4 and 4 (1,023 tokens of 128 query heads: 56 us, 60 with 2 ahead), but with
+            // several axes a unit's angles take registers too (9,001 tokens of 16: 130 us, 86 with 2 ahead).
+            cut = warps_of(4);
+            ahead = AXES ? 2 : 4;
+        } else {
+            // 4 to 12 passes a warp, whatever takes the fewest waves of passes.  A token's first
+            // loads (slot, position, angles, values, one after the other) cost a warp about as
+            // much as six passes, seven with several axes (8 KV and 32 query heads of 128 into
+            // an 8-bit pool, 6 against 12 passes a warp: 1,200 tokens 9.9 and 12.6 us, 2,100 17.0
+            // and 14.6, 9,001 51.4 and 43.7).  Three passes' loads are ahead (80 to 100 registers a
+            // thread, 20 to 24 warps an SM; with six ahead 120 and 16: 9,001 tokens 57.6 us), or all
+            // of four, where as many warps find room (811 tokens 8.5 us, 9.1 with three).
+            int64_t least = INT64_MAX;
+            auto weigh = [&](int c, int un, int64_t room, int more) {
+                const int64_t cost = (((int64_t)p.n * c + room - 1) / room) * ((passes + c - 1) / c + (AXES ? 7 : 6) + more);
+                if (cost <= least) least = cost, cut = c, ahead = un;
+            };
+            for (int c = warps_of(12); c <= warps_of(AXES ? 6 : 4); ++c) {
+                const bool four = !AXES && (passes + c - 1) / c == 4;
+                weigh(c, 3, resident<U, FMT, ROT, 3, AXES>(), four ? 3 : 0);
+                if constexpr (!AXES)
+                    if (four) weigh(c, 4, resident<U, FMT, ROT, 4, AXES>(), 0);
+            }
+            // Six ahead into a bf16 pool while all warps run at once even so (1,100 tokens 7.0 us,
+            // 7.3 with three; into an 8-bit pool 10.0 and 9.8).
+            if constexpr (FMT == rc::kFmtBf16 && !AXES) {
+                const int per = (passes + cut - 1) / cut;
+                if (ahead == 3 && per > 4 && per <= 6 && (int64_t)p.n * cut <= resident<U, FMT, ROT, 6, AXES>()) ahead = 6;
+            }
+        }
     }
     p.per_slice = 32 * ((passes + cut - 1) / cut);
     p.slices = (units + p.per_slice - 1) / p.per_slice;
     const int64_t warps = (int64_t)p.n * p.slices;
     const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return RC_ERR_ARG;
-    if (many) kernel<<<(unsigned)blocks, 32 * kWarps, 0, st>>>(p);
-    else store_rope_kernel<U, FMT, ROT, 1, AXES><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(p);
+    auto go = [&](auto un) { store_rope_kernel<U, FMT, ROT, un(), AXES><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(p); };
+    if (ahead == 1) go(std::integral_constant<int, 1>());
+    else if constexpr (U == 36) go(std::integral_constant<int, AXES ? 2 : 4>());
+    else if (ahead == 3) go(std::integral_constant<int, 3>());
+    else if constexpr (!AXES) {
+        if (ahead == 4) go(std::integral_constant<int, 4>());
+        else if constexpr (FMT == rc::kFmtBf16) go(std::integral_constant<int, 6>());
+    }
     return rc_host::launch_status(cudaGetLastError());
 }
 
