@@ -686,7 +686,8 @@ rc_status beam_select(const void* logits, int32_t logits_f32, int64_t stride, in
  * (start, parents: [batch][beams], first, last: [batch]; all device).  Columns
  * before first[b] are what all beams share; other entries of out are not written.
  * out is table itself (in place) or does not overlap it; the rows' columns must not
- * overlap each other.  max_cols: host bound on last - first (sizes the grid).
+ * overlap each other.  max_cols: host bound on last - first (sizes the grid; any
+ * larger number will do, as no row has more columns than the table entries).
  * table_len: entries of table and of out.  A request with a parent outside
  * 0..beams-1, a row outside the table or more columns than max_cols stays as it is
  * and flags RC_ERR_DEVICE in err (NULL or the device error word).  beams at most

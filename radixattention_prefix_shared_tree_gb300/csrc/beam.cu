@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(128) beam_reorder_kernel(const ReorderParams p
 
 template <int W, int COLS>
 void launch_reorder(const ReorderParams& p, int batch, cudaStream_t st) {
-    const dim3 grid((unsigned)((p.max_cols + 128 * COLS - 1) / (128 * COLS)), (unsigned)batch);
+    const dim3 grid((unsigned)(((int64_t)p.max_cols + 128 * COLS - 1) / (128 * COLS)), (unsigned)batch);
     beam_reorder_kernel<W, COLS><<<grid, 128, 0, st>>>(p);
 }
 
@@ -771,7 +771,10 @@ extern "C" rc_status beam_reorder(const int32_t* table, int32_t* out, int64_t ta
     if (!table || !out || !start || !first || !last || !parents) return RC_ERR_ARG;
     const int64_t apart = reinterpret_cast<const char*>(out) - reinterpret_cast<const char*>(table);
     if (apart != 0 && apart < table_len * 4 && apart > -table_len * 4) return RC_ERR_ARG;  // neither in place nor apart
-    const ReorderParams p{table, out, table_len, start, first, last, parents, beams, max_cols, err};
+    // No row that lies in the table has more columns than it has entries ("no bound" launches no blocks for nothing).
+    const int64_t most = table_len > 1 ? table_len : 1;
+    const ReorderParams p{table, out,     table_len, start, first, last, parents, beams,
+                          (int32_t)(max_cols < most ? max_cols : most), err};
     cudaStream_t st = (cudaStream_t)stream;
     if (beams <= 4) launch_reorder<4, 4>(p, batch, st);
     else if (beams <= 8) launch_reorder<8, 2>(p, batch, st);
