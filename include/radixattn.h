@@ -648,8 +648,9 @@ rc_status attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_
  * aligned).  A bf16 pool's rows are copied bit for bit; of an FP8 pool each value is
  * code times scale rounded to fp32, then to bf16; of a 4-bit pool it is exact.  For a
  * latent pool k_out gets the 576 columns and v_out is NULL.  k_out or v_out may be NULL:
- * not asked for.  A slot may come several times.  One outside [0, n_slots) reads
- * as zeros and flags RC_ERR_DEVICE in pool->err.
+ * not asked for.  They must not overlap the pool's arrays or slots (rows move within a pool
+ * by way of others: kv_load, then kv_store).  A slot may come several times.  One outside
+ * [0, n_slots) reads as zeros and flags RC_ERR_DEVICE in pool->err.
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED (head layouts as kv_store_rope),
  * RC_ERR_CUDA. */
 rc_status kv_load(const rc_pool_desc* pool, const int32_t* slots, int32_t n, void* k_out, int64_t k_stride,

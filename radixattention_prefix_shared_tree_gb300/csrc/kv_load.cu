@@ -174,6 +174,16 @@ extern "C" rc_status kv_load(const rc_pool_desc* pool, const int32_t* slots, int
         return RC_ERR_ARG;
     if (n == 0) return RC_OK;
     if (!slots) return RC_ERR_ARG;
+    const int64_t rows = pool->n_slots * pool->kv_heads;
+    const int64_t bytes = fmt == rc::kFmtBf16 ? rows * D * 2 : fmt == rc::kFmtFp8 ? rows * D : rows * D / 2;
+    for (int i = 0; i < 2; ++i) {  // other blocks may still read what these rows would go over
+        const void* const out = i ? v_out : k_out;
+        const int64_t stride = (i ? v_stride : k_stride) * 2;
+        auto over = [&](const void* in, int64_t size) { return rc_host::overlap(in, size, out, n, stride, row * 2); };
+        if (over(slots, (int64_t)n * 4) || over(pool->k, bytes) || (!pool->mla && over(pool->v, bytes))) return RC_ERR_ARG;
+        if (fmt == rc::kFmtFp8 && (over(pool->k_scale, rows * 4) || over(pool->v_scale, rows * 4))) return RC_ERR_ARG;
+        if (fmt == rc::kFmtFp4 && (over(pool->k_bscale, rows * D / 16) || over(pool->v_bscale, rows * D / 16))) return RC_ERR_ARG;
+    }
     LoadParams p{};
     p.pool[0] = pool->k;
     p.pool[1] = pool->v;

@@ -1,0 +1,41 @@
+"""Refusals of calls at the edge of what the header allows; every call here ends at its
+checks on the host, before any CUDA call."""
+from __future__ import annotations
+
+import torch
+
+import radixattention_prefix_shared_tree_gb300 as ra
+from tests.test_more_operators_host import call_load, pool
+
+BF = torch.bfloat16
+A, OK = ra.RC_ERR_ARG, ra.RC_OK
+
+
+def pools():
+    """A pool of every kind with its arrays' names and sizes in bytes."""
+    n, h, d = 64, 8, 128
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    yield pool(n, h, d), dict(k=n * h * d * 2, v=n * h * d * 2)
+    yield ra.make_pool_desc(torch.zeros(n, 576, dtype=BF), None, mla=True, head_dim_v=512), dict(k=n * 576 * 2)
+    yield (ra.make_pool_desc(u8(n, h, d), u8(n, h, d), k_scale=torch.zeros(n, h), v_scale=torch.zeros(n, h)),
+           dict(k=n * h * d, v=n * h * d, k_scale=n * h * 4, v_scale=n * h * 4))
+    yield (ra.make_pool_desc(u8(n, h, d // 2), u8(n, h, d // 2), k_bscale=u8(n, h, d // 16), v_bscale=u8(n, h, d // 16)),
+           dict(k=n * h * d // 2, v=n * h * d // 2, k_bscale=n * h * d // 16, v_bscale=n * h * d // 16))
+
+
+def test_kv_load_into_its_own_pool_is_refused(built):
+    for p, sizes in pools():
+        latent = bool(p.mla)
+        row = 576 if latent else 1024
+        far = 1 << 40          # (addresses only)
+        base = dict(slots=far, n=4, k=far + (1 << 20), ks=row, v=None if latent else far + (2 << 20), vs=row)
+        ends = [(getattr(p, name), size) for name, size in sizes.items()] + [(far, 16)]
+        for at, size in ends:
+            for out in ("k",) if latent else ("k", "v"):
+                for to in (at, at + size - 16, at - 4 * row * 2 + 16):
+                    to -= to % 16
+                    assert call_load(p, **{**base, out: to}) == A, (sizes, out)
+                # a stride that steps over the array's start: its last row's end is inside
+                assert call_load(p, **{**base, out: at - at % 16 - 3 * 2 * row * 2, out + "s": 2 * row}) == A
+            assert call_load(p, **{**base, "n": 0, "k": at - at % 16}) == OK      # nothing is written
+
