@@ -628,8 +628,8 @@ rc_status attn_cross(const rc_attn_desc* desc, const void* q, const int32_t* qo_
  * q: bf16 rows of q_heads x head_dim, k and v: of kv_heads x head_dim, the rows of
  * neighbouring tokens q_stride, k_stride, v_stride elements apart (multiples of 8,
  * so slices of one projection's output can be passed); out: [n_tokens][q_heads]
- * [head_dim] bf16, not overlapping them; all 16-byte aligned.  lse: NULL or
- * [n_tokens][q_heads] fp32, natural log.  Rows outside every prompt are not written.
+ * [head_dim] bf16; all 16-byte aligned.  lse: NULL or [n_tokens][q_heads] fp32,
+ * natural log.  out and lse must not overlap the inputs or each other.  Rows outside every prompt are not written.
  * The softmax weights are rounded to bf16 as in attn_extend.  What a token does not attend to has no
  * effect on its row, whatever it holds; a NaN in a key that it does makes the row
  * NaN with an lse of +infinity.  err: NULL or the device error word; a prompt whose

@@ -771,11 +771,18 @@ extern "C" rc_status attn_prompt(const void* q, int64_t q_stride, const void* k,
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
          reinterpret_cast<uintptr_t>(out)) & 15)
         return RC_ERR_ARG;
+    const int64_t out_bytes = n_tokens * q_row * 2, lse_bytes = n_tokens * q_heads * 4;
     for (int i = 0; i < 3; ++i) {  // other units may still read what this one's rows would go over
+        const void* const in = i == 0 ? q : i == 1 ? k : v;
         const int64_t stride = i == 0 ? q_stride : i == 1 ? k_stride : v_stride, row = i == 0 ? q_row : kv_row;
-        if (rc_host::overlap(out, n_tokens * q_row * 2, i == 0 ? q : i == 1 ? k : v, n_tokens, stride * 2, row * 2))
+        if (rc_host::overlap(out, out_bytes, in, n_tokens, stride * 2, row * 2) ||
+            rc_host::overlap(lse, lse_bytes, in, n_tokens, stride * 2, row * 2))
             return RC_ERR_ARG;
     }
+    const int64_t ip = ((int64_t)batch + 1) * 4;
+    if (rc_host::overlap(out, out_bytes, indptr, 1, ip, ip) || rc_host::overlap(lse, lse_bytes, indptr, 1, ip, ip) ||
+        rc_host::overlap(lse, lse_bytes, out, 1, out_bytes, out_bytes))
+        return RC_ERR_ARG;
     PromptParams p{};
     p.indptr = indptr;
     p.batch = batch;

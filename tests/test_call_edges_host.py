@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 import radixattention_prefix_shared_tree_gb300 as ra
-from tests.test_more_operators_host import call_load, pool
+from tests.test_more_operators_host import call_load, call_prompt, pool
 
 BF = torch.bfloat16
 A, OK = ra.RC_ERR_ARG, ra.RC_OK
@@ -39,3 +39,14 @@ def test_kv_load_into_its_own_pool_is_refused(built):
                 assert call_load(p, **{**base, out: at - at % 16 - 3 * 2 * row * 2, out + "s": 2 * row}) == A
             assert call_load(p, **{**base, "n": 0, "k": at - at % 16}) == OK      # nothing is written
 
+
+
+def test_attn_prompt_results_over_inputs_are_refused(built):
+    step = 1 << 20      # (addresses only; the arrays below are smaller)
+    far = {n: (1 << 40) + i * step for i, n in enumerate(("q", "k", "v", "ip", "out", "lse"))}
+    size = dict(q=4 * 4096 * 2, k=4 * 1024 * 2, v=4 * 1024 * 2, ip=8, out=4 * 4096 * 2)
+    for name, nbytes in size.items():
+        for to in (far[name], far[name] + nbytes - 4, far[name] - 4 * 32 * 4 + 4):
+            assert call_prompt(**{**far, "batch": 1, "lse": to}) == A, name
+    for to in (far["ip"], far["ip"] - 4 * 4096 * 2 + 16):
+        assert call_prompt(**{**far, "batch": 1, "out": to}) == A
