@@ -654,7 +654,9 @@ def kv_store_rope(pool: rc_pool_desc, rope: rc_rope_desc, slots, positions, k_ne
     header).  k_new, v_new [n, Hkv, d], q, q_out [n, Hq, d]: bf16, each token's
     rows dense, tokens any distance apart; v_new None for a latent pool; q_out
     None rotates q in place.  slots, positions, table_pos: int32 [n]; positions
-    [n_axes, n] where the descriptor has several axes."""
+    [n_axes, n] where the descriptor has several axes.  A descriptor has the axes
+    up to the last that a pair turns by; rows of positions for axes behind it (a
+    model of three axes whose last section is empty) are not read."""
     st = (_host_mod or _host()).kv_store_rope(C.addressof(pool), C.addressof(rope), slots, positions, k_new, v_new, q,
                                               q_out, table, table_pos, stream, pool._dev, rope._dev)
     if st:

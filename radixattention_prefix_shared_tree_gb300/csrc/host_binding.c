@@ -147,7 +147,8 @@ static long long ids(PyObject* t, const char* name, long long n) {
     return sh[0];
 }
 
-/* Positions on several axes: a contiguous int32 tensor [axes, n]. */
+/* Positions on several axes: a contiguous int32 tensor [axes, n], or with rows for further axes (up to 4 in all) behind
+ * them, which no pair turns by. */
 static int axis_ids(PyObject* t, const char* name, long long axes, long long n) {
     const int ok = has_dtype(t, o_i32);
     if (ok < 0) return -1;
@@ -158,8 +159,8 @@ static int axis_ids(PyObject* t, const char* name, long long axes, long long n) 
     if (!c) return -1;
     const int dense = c == Py_True;
     Py_DECREF(c);
-    if (!ok || !dense || nd != 2 || sh[0] != axes || sh[1] != n) {
-        PyErr_Format(PyExc_ValueError, "%s: expected a contiguous int32 tensor [%lld, %lld]", name, axes, n);
+    if (!ok || !dense || nd != 2 || sh[0] < axes || sh[0] > 4 || sh[1] != n) {
+        PyErr_Format(PyExc_ValueError, "%s: expected a contiguous int32 tensor [%lld, %lld] (or of up to 4 axes)", name, axes, n);
         return -1;
     }
     return 0;
@@ -198,8 +199,14 @@ static PyObject* store_rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     const long long hkv = pool->kv_heads, d = pool->head_dim_k;
     const long long n = ids(slots, "slots", -1);
     if (n < 0) return NULL;
-    if (rope->n_axes > 1 ? axis_ids(positions, "positions", rope->n_axes, n) < 0 : ids(positions, "positions", n) < 0)
-        return NULL;
+    int axes = rope->n_axes > 1;
+    if (!axes && rope->pair_axis) { /* all pairs turn by axis 0: [n], or that axis and others */
+        long long sh[4] = {0};
+        const Py_ssize_t nd = as_sizes(PyObject_GetAttr(positions, s_shape), sh);
+        if (nd < 0) return NULL;
+        axes = nd == 2;
+    }
+    if (axes ? axis_ids(positions, "positions", rope->n_axes, n) < 0 : ids(positions, "positions", n) < 0) return NULL;
     if (n > INT32_MAX) {
         PyErr_SetString(PyExc_ValueError, "kv_store_rope: too many tokens");
         return NULL;

@@ -2,6 +2,7 @@
 checks on the host, before any CUDA call."""
 from __future__ import annotations
 
+import pytest
 import torch
 
 import radixattention_prefix_shared_tree_gb300 as ra
@@ -50,3 +51,20 @@ def test_attn_prompt_results_over_inputs_are_refused(built):
             assert call_prompt(**{**far, "batch": 1, "lse": to}) == A, name
     for to in (far["ip"], far["ip"] - 4 * 4096 * 2 + 16):
         assert call_prompt(**{**far, "batch": 1, "out": to}) == A
+
+
+@pytest.mark.parametrize("sections", [[32, 32, 0], [64, 0, 0], [64], [32, 0, 32, 0]])
+def test_positions_may_have_axes_that_no_pair_turns_by(built, sections):
+    rope = ra.make_rope_desc(ra.rope_table(16, 128, device="cpu"), pair_axis=ra.rope_axes(sections))
+    k, s = torch.zeros(4, 8, 128, dtype=BF), torch.zeros(4, dtype=torch.int32)
+
+    def refusal(pos):
+        with pytest.raises((ValueError, RuntimeError)) as e:     # (at the latest because these tensors are the host's)
+            ra.kv_store_rope(pool(), rope, s, pos, k, k)
+        return "expected a contiguous int32" in str(e.value)
+
+    used = max(a for a, n in enumerate(sections) if n) + 1
+    for axes in range(1, 6):
+        assert refusal(torch.zeros(axes, 4, dtype=torch.int32)) == (not used <= axes <= 4), axes
+    assert refusal(s) == (used > 1)
+    assert refusal(torch.zeros(4, 3, dtype=torch.int32)) and refusal(torch.zeros(1, 3, 4, dtype=torch.int32))

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import radixattention_prefix_shared_tree_gb300 as ra
+from tests.test_gpu_pool_rows import make_pool
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -37,3 +38,23 @@ def test_reorder_without_a_bound_on_columns(cuda, w):
                                     par.data_ptr(), b, w, 2 ** 31 - 1, err.data_ptr(), None)
         assert got == ra.RC_OK and ra.rc_sync(err) == st
     assert torch.equal(out, table)
+
+
+@pytest.mark.parametrize("sections", [[32, 32, 0], [64, 0, 0], [20, 0, 44, 0]])
+@pytest.mark.parametrize("n", [1, 300])
+def test_positions_on_an_axis_that_no_pair_turns_by(cuda, sections, n):
+    """A model of three axes whose last section is empty passes its [3, n] positions; the last row has no effect."""
+    g = torch.Generator(device=cuda).manual_seed(n)
+    axis = ra.rope_axes(sections)
+    used, rope = max(axis) + 1, ra.make_rope_desc(ra.rope_table(50, 128, device=cuda), pair_axis=axis)
+    pos = torch.randint(0, 50, (len(sections), n), generator=g, device=cuda).to(torch.int32)
+    pos[used:] = -7
+    k, v = (torch.randn(n, 2, 128, generator=g, device=cuda).to(BF) for _ in range(2))
+    slots = torch.randperm(n, generator=g, device=cuda).to(torch.int32)
+    got = []
+    for p in (pos, pos[:used].contiguous() if used > 1 else pos[0]):
+        pool, arrays, err = make_pool("bf16", n, 2, 128, cuda)
+        ra.kv_store_rope(pool, rope, slots, p, k, v)
+        assert ra.rc_sync(err) == ra.RC_OK
+        got.append(arrays)
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and torch.equal(got[0][1][slots.long()], v)
