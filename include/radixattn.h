@@ -636,7 +636,7 @@ rc_status attn_cross(const rc_attn_desc* desc, const void* q, const int32_t* qo_
  * two entries fall or lie outside 0..n_tokens is left out and flags RC_ERR_DEVICE
  * (where others then overlap, the rows that they share are either's).
  * Errors: RC_ERR_ARG, RC_ERR_UNSUPPORTED (head_dim other than 64 and 128, more than
- * 128 query heads per KV head), RC_ERR_CUDA. */
+ * 128 query heads per KV head, more than 2^20 prompts), RC_ERR_CUDA. */
 rc_status attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, const int32_t* indptr, int32_t batch, int64_t n_tokens,
                       int32_t q_heads, int32_t kv_heads, int32_t head_dim, float sm_scale, void* out,

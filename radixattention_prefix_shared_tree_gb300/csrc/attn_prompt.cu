@@ -55,6 +55,8 @@ constexpr int TM = 128, QT = 2, TN = 128;
 constexpr int BOX = 32;         // rows of K or V a copy
 constexpr int UNITS = 4;        // units known ahead
 constexpr int NB_CACHE = 2048;  // prompts whose block counts are kept in shared memory
+constexpr int FEW = 1024;            // prompts that are looked through again for every unit
+constexpr int MAX_BATCH = 1 << 20;  // every CTA goes through the prompts, about 8 ms each time with so many
 constexpr int THREADS = 384;
 constexpr int COPY_WARP = 8, MMA_WARP = 9, UNIT_WARP = 11;
 constexpr int READERS = 11;  // warps that read a unit: all but its writer
@@ -101,7 +103,10 @@ using tc::ffma2;
 using tc::max3;
 using tc::mbar_arrive;
 
-template <int D>
+// MANY: more prompts than FEW.  (An instance of its own, because what the units' warp does and where
+// its code lies moves the two query tiles against each other: with both ways in one, 3 prompts of 9,000
+// to 14,000 took 6 % longer, 12 of 375 to 1,500 5 %.)
+template <int D, bool MANY>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PromptParams p) {
@@ -607,6 +612,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int b = lane; b < p.batch; b += 32) c += blocks(b) > l;
             return (int)__reduce_add_sync(0xffffffffu, c);
         };
+        // MANY: looked through from the start for every unit, thousands of prompts would take longer
+        // than their work (5,000 of one token, 8 heads of 64: 3,360 us, 1,180 as here; a million, 2
+        // heads: 76 ms).  A level's prompts are gone through once, from b0 on, where its last unit was
+        // found, with `before` of its blocks in front; and counted once for all levels down to `low`,
+        // the next smaller number of blocks that a prompt has.
+        [[maybe_unused]] int low = most, b0 = 0, before = 0;
+        [[maybe_unused]] auto count_down = [&] {
+            int c = 0, next = 0;
+#pragma unroll 8
+            for (int b = lane; b < p.batch; b += 32) {
+                const int x = blocks(b);
+                c += x > lev;
+                next = max(next, x > lev ? 0 : x);
+            }
+            have = (int)__reduce_add_sync(0xffffffffu, c);
+            low = __reduce_max_sync(0xffffffffu, next);
+        };
         auto find = [&](int64_t u) -> Unit {  // (u rises from call to call)
             Unit x{0, -1, 0, 0};
             const int64_t pos = u / p.kv_heads;
@@ -614,9 +636,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             while (pos >= above + have) {
                 above += have;
                 --lev;
-                have = count(lev);
+                if constexpr (MANY) {
+                    b0 = before = 0;
+                    if (lev < low) count_down();
+                } else {
+                    have = count(lev);
+                }
             }
-            int rank = (int)(pos - above), b0 = 0;
+            if constexpr (!MANY) b0 = before = 0;
+            int rank = (int)(pos - above) - before;
             for (;; b0 += 32) {
                 const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < p.batch && blocks(b0 + lane) > lev);
                 const int c = __popc(m);
@@ -625,6 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 rank -= c;
+                if constexpr (MANY) before += c;
             }
             const int b = x.first;
             x.first = __ldg(p.indptr + b);
@@ -718,12 +747,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+template <int D, bool MANY>
+cudaError_t launch(const CUtensorMap (&m)[3], const PromptParams& p, int grid, cudaStream_t st) {
+    cudaError_t e = rc_host::ensure_smem<attn_prompt_kernel<D, MANY>>(smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+    attn_prompt_kernel<D, MANY><<<grid, THREADS, smem_bytes<D>(), st>>>(m[0], m[1], m[2], p);
+    return cudaGetLastError();
+}
 template <int D>
 cudaError_t launch(const CUtensorMap (&m)[3], const PromptParams& p, int grid, cudaStream_t st) {
-    cudaError_t e = rc_host::ensure_smem<attn_prompt_kernel<D>>(smem_bytes<D>());
-    if (e != cudaSuccess) return e;
-    attn_prompt_kernel<D><<<grid, THREADS, smem_bytes<D>(), st>>>(m[0], m[1], m[2], p);
-    return cudaGetLastError();
+    return p.batch > FEW ? launch<D, true>(m, p, grid, st) : launch<D, false>(m, p, grid, st);
 }
 
 }  // namespace
@@ -760,7 +793,7 @@ extern "C" rc_status attn_prompt(const void* q, int64_t q_stride, const void* k,
         return RC_ERR_ARG;
     if (!(sm_scale > 0.f)) return RC_ERR_ARG;  // the largest score has to be the largest scaled one
     const int G = q_heads / kv_heads;
-    if ((head_dim != 64 && head_dim != 128) || G > TM) return RC_ERR_UNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128) || G > TM || batch > MAX_BATCH) return RC_ERR_UNSUPPORTED;
     // reads may overlap (a broadcast row would have stride 0), but a map's strides may not be zero
     const int64_t q_row = (int64_t)q_heads * head_dim, kv_row = (int64_t)kv_heads * head_dim;
     if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || ((q_stride | k_stride | v_stride) & 7) ||

@@ -68,3 +68,8 @@ def test_positions_may_have_axes_that_no_pair_turns_by(built, sections):
         assert refusal(torch.zeros(axes, 4, dtype=torch.int32)) == (not used <= axes <= 4), axes
     assert refusal(s) == (used > 1)
     assert refusal(torch.zeros(4, 3, dtype=torch.int32)) and refusal(torch.zeros(1, 3, 4, dtype=torch.int32))
+
+
+def test_attn_prompt_refuses_more_prompts_than_it_goes_through(built):
+    assert call_prompt(batch=(1 << 20) + 1) == ra.RC_ERR_UNSUPPORTED
+    assert call_prompt(batch=1 << 20, n=0) == OK

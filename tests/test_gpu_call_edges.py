@@ -58,3 +58,49 @@ def test_positions_on_an_axis_that_no_pair_turns_by(cuda, sections, n):
         assert ra.rc_sync(err) == ra.RC_OK
         got.append(arrays)
     assert all(torch.equal(a, b) for a, b in zip(*got)) and torch.equal(got[0][1][slots.long()], v)
+
+
+def prompts_at_once(cuda, lens, hq, hkv, d, seed, err):
+    g = torch.Generator(device=cuda).manual_seed(seed)
+    n = int(lens.sum())
+    q, k, v = (torch.randn(n, h, d, generator=g, device=cuda).to(BF) for h in (hq, hkv, hkv))
+    ip = torch.cat([lens.new_zeros(1), lens]).cumsum(0).to(torch.int32).to(cuda)
+    out, lse = torch.zeros_like(q), torch.zeros(n, hq, device=cuda)
+    ra.attn_prompt(q, k, v, ip, 0.1, out, lse, err)
+    return q, k, v, ip, out, lse
+
+
+@pytest.mark.parametrize("batch,most,hq,hkv,d", [(1024, 2, 8, 2, 64), (1025, 700, 4, 2, 64), (2049, 3, 4, 4, 64),
+                                                 (5000, 2, 4, 1, 128), (3000, 400, 8, 8, 64), (40, 5000, 8, 2, 128)])
+def test_very_many_prompts(cuda, batch, most, hq, hkv, d):
+    """Thousands of prompts of all lengths (none among them), one much longer: a prompt's rows do not depend on the
+    others in its batch, so they are, bit for bit, those of the same prompts a few at a time."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, most + 1, (batch,), generator=g)
+    lens[torch.rand(batch, generator=g) < 0.2] = 0
+    lens[batch // 3] = 3001
+    err = torch.zeros(1, dtype=torch.int32, device=cuda)
+    q, k, v, ip, out, lse = prompts_at_once(cuda, lens, hq, hkv, d, batch, err)
+    few_out, few_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    for a in range(0, batch, 100):
+        ra.attn_prompt(q, k, v, ip[a:a + 101], 0.1, few_out, few_lse, err)
+    assert ra.rc_sync(err) == ra.RC_OK
+    assert torch.equal(out, few_out) and torch.equal(lse, few_lse)
+    assert bool((lse != 0).any(1).all())
+
+
+def test_time_follows_the_number_of_prompts(cuda):
+    """100,000 prompts of a token, then as many of none but a few: a prompt is looked for once a level, not once a unit
+    (which took 100 times as long as the limit here)."""
+    err = torch.zeros(1, dtype=torch.int32, device=cuda)
+    for lens in (torch.ones(100_000, dtype=torch.int64), (torch.arange(100_000) % 5000 == 4999).long() * 700):
+        prompts_at_once(cuda, lens, 8, 8, 64, 1, err)
+        assert ra.rc_sync(err) == ra.RC_OK
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        q, k, v, ip, out, lse = prompts_at_once(cuda, lens, 8, 8, 64, 2, err)
+        b.record()
+        assert ra.rc_sync(err) == ra.RC_OK
+        assert a.elapsed_time(b) < 200, "ms"
+        if bool((lens == 1).all()):     # a token alone: its own value
+            assert torch.equal(out, v)
