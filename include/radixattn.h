@@ -630,7 +630,8 @@ rc_status attn_cross(const rc_attn_desc* desc, const void* q, const int32_t* qo_
  * so slices of one projection's output can be passed); out: [n_tokens][q_heads]
  * [head_dim] bf16; all 16-byte aligned.  lse: NULL or [n_tokens][q_heads] fp32,
  * natural log.  out and lse must not overlap the inputs or each other.  Rows outside every prompt are not written.
- * The softmax weights are rounded to bf16 as in attn_extend.  What a token does not attend to has no
+ * The softmax weights are rounded to bf16, as attn_extend does over bf16 pools (over pools of codes
+ * it keeps f16, three bits more).  What a token does not attend to has no
  * effect on its row, whatever it holds; a NaN in a key that it does makes the row
  * NaN with an lse of +infinity.  err: NULL or the device error word; a prompt whose
  * two entries fall or lie outside 0..n_tokens is left out and flags RC_ERR_DEVICE

@@ -521,7 +521,10 @@ class DeviceEngine:
         cached): attn_prompt reads the new tokens' K and V as they are, dense,
         instead of gathering them by slot.  Call store first; a pool of codes is
         read back (kv_load), so that the prompt sees the values that its later
-        steps will.  GQA layouts."""
+        steps will: exactly those of a 4-bit pool, those of an E4M3 pool rounded to
+        bf16.  The softmax weights are rounded to bf16 (8 bits) over every pool,
+        where extend and the decode steps keep f16 (11) over pools of codes: use
+        extend where a prompt's last bits matter more than its time.  GQA layouts."""
         if int(lay.first.max(initial=0)) > 0 or self.shape.mla:
             raise ValueError("prompt() computes whole prompts of a GQA layout: use extend()")
         if self.kv_fp8 or self.kv_fp4:

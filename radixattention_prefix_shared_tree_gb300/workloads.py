@@ -40,7 +40,8 @@ class Runner:
         self.cascade = cascade
         self.collect = collect
         self.prefill_attention = prefill_attention
-        # batches of which nothing is cached: attention over the prompts as they lie (DeviceEngine.prompt)
+        # batches of which nothing is cached: attention over the prompts as they lie (DeviceEngine.prompt,
+        # which over pools of codes rounds to fewer bits than extend)
         self.whole_prompts = whole_prompts
         self.extend_out = {}   # rid -> (positions, out bf16 [n, Hq, dv], lse [n, Hq])
         self.decode_out = {}   # rid -> list of (position, out [Hq, dv], lse [Hq])

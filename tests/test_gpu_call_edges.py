@@ -1,10 +1,18 @@
 """Calls at the edge of what the header allows: the largest bounds, unused axes, very many prompts."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 import radixattention_prefix_shared_tree_gb300 as ra
+from oracle import fp4_oracle as f4
+from radixattention_prefix_shared_tree_gb300 import workloads as wl
+from radixattention_prefix_shared_tree_gb300.driver import DeviceEngine
+from synth import hashgen as hg
+from synth.model import SynthModel
+from tests import tolerance as tol
+from tests.test_gpu_generation import shape_of, values
 from tests.test_gpu_pool_rows import make_pool
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +112,29 @@ def test_time_follows_the_number_of_prompts(cuda):
         assert a.elapsed_time(b) < 200, "ms"
         if bool((lens == 1).all()):     # a token alone: its own value
             assert torch.equal(out, v)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("lens", [[400, 1, 77], [1300]])
+def test_whole_prompts_over_pools_of_codes_vs_oracle(cuda, fmt, lens):
+    """DeviceEngine.prompt against the oracle over the values that it reads back: the pool's own of 4 bits, those
+    of an E4M3 pool rounded to bf16, with the softmax weights in bf16; extend over the same tokens against the
+    pool's own values, with the weights in f16."""
+    sh, pool = shape_of(), 4000
+    model = SynthModel(sh, 5, 500, device=cuda)
+    for whole in (True, False):
+        eng = DeviceEngine(sh, pool, cuda, kv_fp8=fmt == "fp8", kv_fp4=fmt == "fp4")
+        runner = wl.Runner(ra.RadixCache(pool), model, eng, collect=True, whole_prompts=whole)
+        reqs = [runner.request((np.arange(n) * (i + 3) % 500).astype(np.int32), 1) for i, n in enumerate(lens)]
+        runner.serve(reqs)
+        assert ra.rc_sync(eng.err) == ra.RC_OK
+        for r in reqs:
+            h = hg.prefix_hashes(r.prompt, model.seed)
+            q = hg.bf16_bits_to_f32(hg.gen_values(h, hg.KIND_Q, sh.q_heads, sh.head_dim_k)).astype(np.float64)
+            kv = values(fmt, eng, sh, h)
+            if whole:
+                kv = [hg.bf16_bits_to_f32(f4.bf16_round(x.astype(np.float32))).astype(np.float64) for x in kv]
+            o, t, a = f4.attention(q, *kv, [np.arange(i + 1) for i in range(len(h))], sh.q_heads, sh.kv_heads, sh.scale)
+            _, out, lse = runner.extend_out[r.rid]
+            tol.check_values(hg.bf16_bits_to_f32(out).astype(np.float64), o, a, u_p=tol.U_BF16 if whole else tol.U_F16)
+            tol.check_lse(lse, t)
