@@ -138,3 +138,24 @@ def test_whole_prompts_over_pools_of_codes_vs_oracle(cuda, fmt, lens):
             _, out, lse = runner.extend_out[r.rid]
             tol.check_values(hg.bf16_bits_to_f32(out).astype(np.float64), o, a, u_p=tol.U_BF16 if whole else tol.U_F16)
             tol.check_lse(lse, t)
+
+
+@pytest.mark.parametrize("hkv,d,n", [(4, 128, 64), (3, 64, 5000)])
+def test_rows_of_4_bits_move_between_pools(cuda, hkv, d, n):
+    """Rows of a 4-bit pool, read back and stored in another, are the same codes and scales: their values are exact in
+    bf16, and the largest of a block is 6 scales (a scale of four bits is within 2^-4 of amax / 6, so that amax is at
+    least 5.6 of them and its code 6), so that the block gets its scale again.  Zeros of either sign and blocks
+    with a NaN likewise.  (Blocks below 6 x 2^-14, whose scales go in steps of 2^-17, need not.)"""
+    g = torch.Generator(device=cuda).manual_seed(n)
+    src, had, err = make_pool("fp4", n, hkv, d, cuda)
+    spread = torch.exp2(torch.randint(-8, 9, (n, hkv, 1), generator=g, device=cuda).float())
+    k, v = ((torch.randn(n, hkv, d, generator=g, device=cuda) * spread).to(BF) for _ in range(2))
+    k[1], k[2], k[3, :, 5] = 0.0, -0.0, float("nan")
+    every = torch.randperm(n, generator=g, device=cuda).to(torch.int32)
+    ra.kv_store(src, every, k, v)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    ra.kv_load(src, every, ko, vo)
+    dst, got, err2 = make_pool("fp4", n, hkv, d, cuda, fill=7)
+    ra.kv_store(dst, every, ko, vo)
+    assert ra.rc_sync(err) == ra.RC_OK and ra.rc_sync(err2) == ra.RC_OK
+    assert all(torch.equal(a, b) for a, b in zip(had, got))
