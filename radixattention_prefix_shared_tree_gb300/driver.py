@@ -822,6 +822,8 @@ class BeamBatch:
         private = np.asarray(plan["private"], np.int64).reshape(B, W)[:, 0]    # equal rows: equal for a request's beams
         own = np.fromiter((r.prompt_len for r in batch), np.int64, B) - private
         room = int(own.max(initial=0)) + T
+        if B * W * room >= 2 ** 31:    # (places in the table are 32 bits wide)
+            raise ValueError(f"BeamBatch: {B} x {W} rows of {room} slots are more than a table holds: take fewer requests at once")
         table = np.zeros((B * W, room), np.int32)
         for b, p in enumerate(prompts):
             table[b * W:(b + 1) * W, :own[b]] = p[private[b]:]

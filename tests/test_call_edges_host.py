@@ -2,10 +2,14 @@
 checks on the host, before any CUDA call."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
+import numpy as np
 import pytest
 import torch
 
 import radixattention_prefix_shared_tree_gb300 as ra
+from radixattention_prefix_shared_tree_gb300.driver import BeamBatch
 from tests.test_more_operators_host import call_load, call_prompt, pool
 
 BF = torch.bfloat16
@@ -73,3 +77,12 @@ def test_positions_may_have_axes_that_no_pair_turns_by(built, sections):
 def test_attn_prompt_refuses_more_prompts_than_it_goes_through(built):
     assert call_prompt(batch=(1 << 20) + 1) == ra.RC_ERR_UNSUPPORTED
     assert call_prompt(batch=1 << 20, n=0) == OK
+
+
+def test_beam_batch_refuses_a_table_past_32_bits(built):
+    """Latent rows have no shared segments, so that every beam's row names its whole prompt."""
+    eng = SimpleNamespace(shape=SimpleNamespace(mla=True), torch=torch)
+    n = 2 ** 31 // 32 - 4     # (slots without memory of their own)
+    r = SimpleNamespace(rid=0, prompt_len=n, slots=np.broadcast_to(np.int32(0), (n + 32 * 4,)))
+    with pytest.raises(ValueError, match="1 x 32 rows"):
+        BeamBatch(eng, [r], 32, 4)
