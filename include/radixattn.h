@@ -663,10 +663,14 @@ rc_status kv_load(const rc_pool_desc* pool, const int32_t* slots, int32_t n, voi
  * probabilities.  A continuation (w, v) of request b scores
  *   scores[b][w] + logits[b][w][v] - log sum_u exp(logits[b][w][u]);
  * the n_out best of all beams go to out_scores, out_tokens (v) and out_parents (w),
- * [batch][n_out] each, best first, equal scores by (w, v).  They are ranked by
- * scores of 48 bits, before these are rounded (how a row is split, and so the last bits of
- * its sum, depends on the sizes of the call).  A logit of -infinity is no continuation (a mask); where there are
- * fewer than n_out, the rest has score -infinity, token 0, parent 0.
+ * [batch][n_out] each, best first, equal scores by (w, v).  They are ranked
+ * before the scores are rounded to fp32: one beam's by their logits, exactly; different
+ * beams' by scores as good as the sums in them, 2^-20, so that nearer ones may come in
+ * either order (and in another one as part of a call of other sizes, which splits the rows
+ * differently).  A logit of -infinity is no continuation (a mask); where there are fewer
+ * than n_out, the rest has score -infinity, token 0, parent 0.  (A finite lowest value as a
+ * mask is a logit like others: where more than a thousand equal ones of a row have to fill
+ * places, the row is read again for every place.)
  * done: NULL or [batch][beams]: a beam that is done (non-zero) has one
  * continuation, end_token at no cost, and its logits are not read.  out_done: NULL or
  * [batch][n_out]: whether the parent was done or the token is end_token (-1: none).

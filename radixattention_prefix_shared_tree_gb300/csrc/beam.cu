@@ -23,8 +23,11 @@
 // Ties: equal scores go to the lowest (beam, token).  A logit and its token make one
 // 64-bit key (the logit's order above, the token's complement below), so no two are
 // equal and no order of collecting them matters.  Between the beams scores of two
-// 32-bit words (48 bits) rank, because beams' near scores decide which one lives; 64-bit
-// arithmetic takes about 100 cycles an operation here.
+// 32-bit words rank, because beams' near scores decide which one lives and fp32's step at
+// a score of 10 is 1e-6; 64-bit arithmetic takes about 100 cycles an operation here.  They are
+// as good as the log-sum-exps in them: 2^-20 (fp32 arguments and results of ex2, a thread's
+// sums and its factor expf(m - top)), 1.6e-7 at most as measured, so nearer scores of two beams may come
+// in either order.  Within a beam the order is exact.
 
 #include "tc.cuh"
 
@@ -483,7 +486,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) beam_select_kernel(const Select
             }
             for (int i = n_keys + t; i < K; i += kThreads) send(cs, to + i, 0);
         } else {
-            // more than there is room for (many equal logits): one after the other, the largest below the last
+            // more than there is room for (many equal logits): one after the other, the largest below the last.
+            // K passes over the row: with all but five logits at fp32's lowest value 64 x 8 x 32,000, K = 16, takes
+            // 294 us (20 with them at -infinity), 200 x 4 x 32,003 bf16, K = 64, 1.6 ms
             Key last = ~0ull;
             for (int k = 0; k < K; ++k) {
                 Key best = 0;

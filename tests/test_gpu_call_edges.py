@@ -159,3 +159,28 @@ def test_rows_of_4_bits_move_between_pools(cuda, hkv, d, n):
     ra.kv_store(dst, every, ko, vo)
     assert ra.rc_sync(err) == ra.RC_OK and ra.rc_sync(err2) == ra.RC_OK
     assert all(torch.equal(a, b) for a, b in zip(had, got))
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("v,gain", [(500, 4.0), (7142, 1.0), (32_000, 4.0), (130_001, 1.0)])
+def test_select_scores_before_their_rounding(cuda, v, gain, f32):
+    """A beam's score and its best logit that all but cancel the log-sum-exp leave the latter's error: at most 2^-20.
+    Terms are off by 2^-22 (ex2) and, from their arguments' rounding, by ln 2 |y| 2^-24 where y is the exponent (8 on
+    the weighted average here: 2^-21.5), a thread's eight terms at a time by 3 x 2^-24, its factor by 2^-23 (9.2e-7
+    in all), and what the calls of one row and of all rows differ by is at most twice that."""
+    g = torch.Generator(device=cuda).manual_seed(v)
+    x = (torch.randn(96, 1, v, generator=g, device=cuda) * gain).to(torch.float32 if f32 else BF)
+    lse, top = torch.logsumexp(x.double(), -1), x.double().max(-1).values
+    s = (lse - top).float()
+    exact = s.double() + top - lse
+
+    def best(a, b):
+        out = torch.empty(b - a, 1, device=cuda)
+        tok, par = (torch.empty(b - a, 1, dtype=torch.int32, device=cuda) for _ in range(2))
+        ra.beam_select(x[a:b], s[a:b], out, tok, par)
+        return out.double()
+
+    every, alone = best(0, 96), torch.cat([best(i, i + 1) for i in range(96)])
+    assert (every - exact).abs().max().item() <= 2.0 ** -20
+    assert (alone - exact).abs().max().item() <= 2.0 ** -20
+    assert (every - alone).abs().max().item() <= 2.0 ** -19
