@@ -25,10 +25,12 @@
 // that one's products run under the other's softmax.  CTAs are persistent, one an SM;
 // unit u+1's copies and its first product run while unit u's rows are written.
 //
-// Measured: 3 prompts of 9,000 to 14,000 tokens, 32/8 heads of 128: 1,740 us, 1,560
-// TFLOP/s of the products a causal mask leaves, bound by the tensor core (cuBLAS keeps up
-// 1,725).  One of 2,049, 64/8 heads: 69 us.  256 prompts of 128 to 512: 508 us, 3.3 TB/s, bound by the chain of a unit
-// (loads, two to five tiles, rows out).  12 of 375 to 1,500, 16 heads of 64: 58.5 us.
+// Measured: 3 prompts of 9,000 to 14,000 tokens, 32/8 heads of 128: 1,690 to 1,860 us from GPU to
+// GPU, 1,460 to 1,610 TFLOP/s of the products a causal mask leaves, bound by the tensor core (cuBLAS
+// keeps up 1,725).  One of 2,049, 64/8 heads: 69 us.  256 prompts of 128 to 512: 508 us, 3.3
+// TB/s, bound by the chain of a unit (loads, two to five tiles, rows out).  12 of 375 to 1,500,
+// 16 heads of 64: 58.5 us.  At the 168 registers that twelve warps leave each thread, head
+// dimension 64 spills 36 bytes a thread, 128 52.
 // Tried and slower: results by four warps of their own with TMA stores (sixteen warps:
 // 556 us for the short prompts), a softmax of two passes over S instead of 128 scores in
 // registers (2,145 us for the long ones), a lock around a tile's products (528 us for the

@@ -15,8 +15,8 @@
 // and hardly more do (n_out = 16: 22 of any number), and only the words whose maximum
 // reaches it are read again (from L2).  What reaches the bar is ranked by counting.
 // The first CTA of the cluster ranks the rows' lists together.  Measured: 64 requests of
-// 8 beams, 32,000 fp32 logits, n_out 16, 20.0 us (3.3 TB/s); 1 x 4 x 32,000 bf16, 6.8 us; 200 x 4 x
-// 32,003 bf16, 21.9 us (2.3 TB/s): a row's stages wait for one another (barriers and loads are
+// 8 beams, 32,000 fp32 logits, n_out 16, 20.2 us (3.2 TB/s); 1 x 4 x 32,000 bf16, 7.0 us; 200 x 4 x
+// 32,003 bf16, 21.7 us (2.4 TB/s): a row's stages wait for one another (barriers and loads are
 // most of the stalls), and at 64 registers a thread an SM has 1,024 threads to fill the gaps.
 // beam_reorder, 200 x 4 rows of 2,000 columns: 4.0 us.
 //
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kMaxBeams = 32, kMaxOut = 64, kMaxCluster = 8, kWideCluster = 16;
 constexpr int UN = 2;             // words a thread has on their way (4, with three CTAs an SM instead of four: 64 x 8 rows
-                                  // of 32,000 fp32 took 27.6 us instead of 22.3)
+                                  // of 32,000 fp32 took a quarter longer)
 constexpr int kBlocks = 8;        // runs of groups whose maxima are kept, at most
 constexpr int kKeys = 1024, kPairs = 1024;
 
@@ -738,7 +738,8 @@ extern "C" rc_status beam_select(const void* logits, int32_t logits_f32, int64_t
     p.cluster = beams < kMaxCluster ? beams : kMaxCluster;
     if (beams > kMaxCluster) {
         // up to 16 CTAs a request, while they all run at once (more than 8 have to find room in one part of
-        // the chip): 1 x 16 x 32,000 bf16, n_out 32, 18.3 us, 23.7 with 8; 50 x 32 x 32,000 120 and 112
+        // the chip): 16 and 8 CTAs, 1 x 16 x 32,000 bf16, n_out 32, 14.7 and 20.1 us, 8 x 10 x 50,257 fp32,
+        // n_out 20, 24.5 and 43.4; beyond, 50 x 32 x 32,000 bf16, n_out 32 66.1 and 58.6, n_out 64 169 and 113
         const int most = beams < kWideCluster ? beams : kWideCluster;
         if ((int64_t)batch * most <= 4 * (int64_t)rc_host::sm_count()) p.cluster = most;
     }

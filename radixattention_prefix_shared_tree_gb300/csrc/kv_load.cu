@@ -9,11 +9,12 @@
 // codes with their scale byte, or 16 of E4M3 codes; consecutive lanes take
 // consecutive values.  A warp takes UN runs of 32 such units, all loads before the
 // first use: one while all threads run at once, which is the shorter way for few tokens, two
-// beyond (8 KV heads of 128, 1, 2, 4 and 8 of them: 27 tokens of E4M3 2.75, 3.2, 3.4 and 4.4 us,
-// 60,001 of 4 bits 60.7, 53.3, 57.5 and 67.5).
-// Measured: 60,001 tokens, 8 KV heads of 128, 4 bits, 51.6 us, 6.1 TB/s of what is read and
-// written (a copy does 6.8); 1,792 tokens of E4M3, 3.9 us, of which 0.8 is an empty
-// launch's: the slot, then code and scale, then the store wait for one another.
+// beyond (8 KV heads of 128, 1, 2, 4 and 8 of them, a call among others: 27 tokens of E4M3 2.75,
+// 3.2, 3.4 and 4.4 us, 60,001 of 4 bits 60.7, 53.3, 57.5 and 67.5).
+// Measured (from a graph): 60,001 tokens, 8 KV heads of 128, 4 bits 51.1 us, 6.2 TB/s of what is
+// read and written (a copy does 6.8), E4M3 57.8, bf16 73.5, latent rows 23.0; 1,792 tokens of
+// E4M3 3.7 us, of which 0.8 is an empty launch's: the slot, then code and scale, then the store
+// wait for one another.
 
 #include "common.cuh"
 

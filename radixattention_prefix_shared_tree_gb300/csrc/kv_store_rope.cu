@@ -88,7 +88,7 @@ RC_DEV float block_scale_value(uint32_t byte) {
 // and its quotient, rounded to fp32, is not T either.  So any quotient good to a step
 // decides as the exact one does, if it is T where x = T s: q of 12 bits, whose product
 // with s is exact, plus the remainder (exact, too) over s.  (16 divisions a thread
-// instead: 71 us for 9,001 tokens, against 64.)
+// instead: 46.6 us for 9,001 tokens of 8 KV and 32 query heads of 128, against 43.9.)
 RC_DEV uint32_t e2m1_codes(const float (&x)[8], uint32_t byte) {
     if (byte == 0u || byte == 0xffu) return 0u;
     const float s = block_scale_value(byte), r = __frcp_rn(s);
