@@ -1,6 +1,9 @@
 """Calls at the edge of what the header allows: the largest bounds, unused axes, very many prompts."""
 from __future__ import annotations
 
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +15,7 @@ from radixattention_prefix_shared_tree_gb300.driver import DeviceEngine
 from synth import hashgen as hg
 from synth.model import SynthModel
 from tests import tolerance as tol
+from tests.conftest import ROOT
 from tests.test_gpu_generation import shape_of, values
 from tests.test_gpu_pool_rows import make_pool
 
@@ -98,8 +102,8 @@ def test_very_many_prompts(cuda, batch, most, hq, hkv, d):
 
 
 def test_time_follows_the_number_of_prompts(cuda):
-    """100,000 prompts of a token, then as many of none but a few: a prompt is looked for once a level, not once a unit
-    (which took 100 times as long as the limit here)."""
+    """100,000 prompts of a token, then as many of none but a few: a prompt is looked for once a level (25 ms), not once
+    a unit (3.4 ms for 5,000 prompts, and that grew with the square of their number)."""
     err = torch.zeros(1, dtype=torch.int32, device=cuda)
     for lens in (torch.ones(100_000, dtype=torch.int64), (torch.arange(100_000) % 5000 == 4999).long() * 700):
         prompts_at_once(cuda, lens, 8, 8, 64, 1, err)
@@ -184,3 +188,40 @@ def test_select_scores_before_their_rounding(cuda, v, gain, f32):
     assert (every - exact).abs().max().item() <= 2.0 ** -20
     assert (alone - exact).abs().max().item() <= 2.0 ** -20
     assert (every - alone).abs().max().item() <= 2.0 ** -19
+
+
+FIRST_CALLS = """
+import torch
+import radixattention_prefix_shared_tree_gb300 as ra
+BF, dev = torch.bfloat16, torch.device("cuda")
+n, ints = {n}, dict(dtype=torch.int32, device=dev)
+k, v, q = (torch.randn(n, h, 128, device=dev).to(BF) for h in (8, 8, 32))
+pools = [[torch.zeros(n, 8, 128, dtype=BF, device=dev) for _ in range(2)] for _ in range(2)]
+descs, rope = [ra.make_pool_desc(*p) for p in pools], ra.make_rope_desc(ra.rope_table(n, 128, device=dev))
+at, ip = torch.arange(n, **ints), torch.arange(0, n + 1, max(n // {prompts}, 1), **ints)
+outs = [[torch.zeros_like(x) for x in (q, k, v, q)] for _ in range(2)]
+
+
+def calls(desc, o):
+    ra.kv_store_rope(desc, rope, at, at, k, v, q, o[0])
+    ra.kv_load(desc, at, o[1], o[2])
+    ra.attn_prompt(o[0], o[1], o[2], ip, 0.1, o[3])
+
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls(descs[0], outs[0])
+g.replay()
+calls(descs[1], outs[1])
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(*outs)) and bool(outs[0][3].any())
+"""
+
+
+@pytest.mark.parametrize("n,prompts", [(1, 1), (1100, 1100), (4001, 3)])
+def test_first_calls_of_a_process_are_captured(cuda, n, prompts):
+    """What a call asks the driver about its kernels the first time may be asked while a graph is captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(n=n, prompts=prompts)], capture_output=True, text=True,
+                       timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
